@@ -61,7 +61,8 @@ typedef enum {
   NC_E_ARG = 1,          /* null pointer, negative size, bad policy field */
   NC_E_ALIGN = 2,        /* element pointer not 16-byte aligned */
   NC_E_SHAPE = 3,        /* MX: cols not a positive multiple of 32, n % cols != 0, rows not a
-                            multiple of 32 for NC_MX_COLS, or mixed mx_axis in one call */
+                            multiple of 32 for NC_MX_COLS, or mixed mx_axis in one call; cache:
+                            page not a positive multiple of 16, q_heads not a multiple of heads */
   NC_E_UNSUPPORTED = 4,  /* unknown enum value */
   NC_E_HIP = 5,          /* a HIP launch failed */
   NC_E_WORKSPACE = 6,    /* workspace missing or smaller than nc_workspace_bytes() */
@@ -69,7 +70,9 @@ typedef enum {
 } nc_status;
 
 typedef enum { NC_F32 = 0, NC_BF16 = 1 } nc_dtype;
-typedef enum { NC_E4M3 = 0, NC_E5M2 = 1 } nc_fmt;
+/* E2M1 (4 bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) is a format of the
+ * key/value cache only. */
+typedef enum { NC_E4M3 = 0, NC_E5M2 = 1, NC_E2M1 = 2 } nc_fmt;
 
 /* MX shared-exponent rules for a block with finite amax a = m * 2^e, m in [1,2)
  * ([Drift, "What the measurements said" and "The part I would rather not
@@ -364,6 +367,109 @@ nc_status nc_swamp_watch(const nc_update_tensor *t, int32_t count, nc_wfmt wfmt,
  * else 0; promoted = promoted or run >= window; steps += 1. */
 nc_status nc_swamp_window(const nc_swamp_policy *policy, int32_t count, nc_swamp_state *st,
                           const nc_swamp_counts *in, void *stream);
+
+/* ---- The key/value cache ------------------------------------------------------
+ * Keys and values of past tokens, held as MX blocks in pages and attended over
+ * without being brought back first.  A token's row of one head has `dim`
+ * elements; 32 consecutive ones share X by nc_mx_rule (the largest value 6 for
+ * E2M1, 448 for E4M3) and round as in nc_cast_mx.  A token lives at a slot,
+ * page * c.page + offset.  Bytes of a token and head: dim / 2 (E2M1) or dim
+ * (E4M3), and dim / 32, for each of key and value.
+ *
+ * What a cache holds of a value that is not finite: +-Inf becomes +-max; a NaN
+ * becomes 0x7F in E4M3; E2M1 has no NaN, so its whole block gets scale byte 255
+ * and reads as NaN.  The byte order inside `data` belongs to the library; a
+ * cache of zero bytes holds zeros.  A page is whole: pages may be copied,
+ * moved and shared between sequences (nc_kv_cache_bytes(1, ...) bytes each,
+ * page p at p times that). */
+typedef struct {
+  uint8_t *data;    /* (device) nc_kv_cache_bytes() bytes, 16-byte aligned */
+  int64_t pages;    /* >= 0; pages * page and pages * page / 16 * heads below 2^31 */
+  int32_t page;     /* tokens of a page, a positive multiple of 16 */
+  int32_t heads;    /* key/value heads, 1 .. 65536 */
+  int32_t dim;      /* 64, 96, 128, 192 or 256 */
+  int32_t fmt;      /* NC_E2M1 or NC_E4M3 */
+} nc_kv_cache;
+
+/* Rows in memory: element (token, head, i) at data[token * token_stride +
+ * head * head_stride + i].  data is 16-byte aligned and both strides are
+ * multiples of 16 bytes (counted in elements, >= 0). */
+typedef struct {
+  void *data;       /* (device) */
+  int64_t token_stride;
+  int64_t head_stride;
+} nc_kv_rows;
+
+/* Bytes of a cache's data; 0 for sizes that nc_kv_cache does not allow. */
+size_t nc_kv_cache_bytes(int64_t pages, int32_t page, int32_t heads, int32_t dim, int32_t fmt);
+
+/* Writes `tokens` rows of keys and values (c->heads heads each) at slots[i]
+ * (device, int64).  A slot outside [0, pages * page) is skipped (-1 marks
+ * padding); the slots of one call are distinct.  Each token is written on its
+ * own: other tokens of its page keep their bytes. */
+nc_status nc_kv_write(const nc_kv_cache *c, const nc_kv_rows *k, const nc_kv_rows *v, int64_t tokens,
+                      nc_dtype dtype, const int64_t *slots, nc_mx_rule rule, void *stream);
+
+/* Reads the rows at slots[i] back: y = decode(q) * 2^X, exact in fp32 (rounded
+ * to nearest even below its normal range) and in bf16 (the same).  A slot
+ * outside the cache reads as zeros. */
+nc_status nc_kv_read(const nc_kv_cache *c, const nc_kv_rows *k, const nc_kv_rows *v, int64_t tokens,
+                     nc_dtype dtype, const int64_t *slots, void *stream);
+
+/* One attention call over a batch of sequences.  Sequence b has the queries
+ * q_start[b] .. q_start[b + 1] - 1 (rows of q) and kv_len[b] cached tokens;
+ * token t is at offset t % page of page table[b * table_pages + t / page].
+ * Query head j attends to cache head j / (q_heads / heads).
+ *
+ * The i-th of n_q queries sees the tokens t < end and, with a window,
+ * t >= end - window, where end = kv_len[b] - n_q + 1 + i with `causal` (the
+ * queries are the last n_q cached tokens) and kv_len[b] without (cross
+ * attention: the cache holds an encoder's tokens).  Over those,
+ *   out = sum_t softmax_t(scale * q.k_t) v_t,  lse = log sum_t exp(scale * q.k_t);
+ * a query that sees none gets out = 0 and lse = -inf.
+ *
+ * The arrays in device memory are not trusted: kv_len is cut to max_kv and to
+ * what the table holds, a negative one counts as 0, more than max_q queries
+ * are cut, q_start that decreases or passes total_q gives that sequence no
+ * queries (its rows of out are left as they were), and tokens on a page
+ * outside the cache are not seen.
+ *
+ * A cached NaN that a query sees makes its lse and out NaN (of a value: the
+ * elements concerned).  Tokens past kv_len may hold anything. */
+typedef struct {
+  const void *q;            /* (device) total_q rows of q_heads heads, dtype fp32 or bf16 */
+  int64_t q_token_stride, q_head_stride;
+  void *out;                /* (device) as q, of the same dtype */
+  int64_t out_token_stride, out_head_stride;
+  float *lse;               /* (device, nullable) lse[row * lse_token_stride + head] */
+  int64_t lse_token_stride;
+  const int32_t *q_start;   /* (device) batch + 1 */
+  const int32_t *kv_len;    /* (device) batch */
+  const int32_t *table;     /* (device) batch x table_pages page numbers */
+  int32_t table_pages;
+  int32_t batch;
+  int32_t total_q;          /* rows of q, out and lse */
+  int32_t q_heads;          /* a multiple of the cache's heads */
+  int32_t max_q;            /* no sequence has more queries (host: sets the grid) */
+  int32_t max_kv;           /* nor more cached tokens */
+  int32_t causal;           /* 0/1 */
+  int32_t window;           /* tokens that a query sees at most; 0: no window */
+  float scale;              /* finite; 1 / sqrt(dim) is usual */
+} nc_kv_attn;
+
+/* bf16 calls round the softmax weights to bf16 before the product with the
+ * values, fp32 calls keep them whole; scores, maxima, sums and products are
+ * fp32.  Long caches are cut along the tokens over the workgroups; the
+ * partial sums go through ws (nc_kv_workspace_bytes() bytes, 16-byte aligned,
+ * no initialisation; NULL when that is 0) and meet in a fixed order: the same
+ * call gives the same bits. */
+nc_status nc_kv_attention(const nc_kv_cache *c, const nc_kv_attn *a, nc_dtype dtype, void *ws, size_t ws_bytes,
+                          void *stream);
+
+/* Workspace of nc_kv_attention for these sizes, whatever the mask; it does not
+ * read c->data. */
+size_t nc_kv_workspace_bytes(const nc_kv_cache *c, nc_dtype dtype, int32_t q_heads, int32_t batch, int32_t max_q,
+                             int32_t max_kv);
 
 #ifdef __cplusplus
 }

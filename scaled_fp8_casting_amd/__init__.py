@@ -14,18 +14,22 @@ Device buffers used by the calls, as torch tensors:
 * state:  int32 [count, 6] -- k, a_ref bits, has_ref, n_hist, head, step;
 * hist:   float32 [count, window];
 * loss scale: int32 [2] -- s_log2, clean_steps.
+
+The key/value cache (new_kv_cache, nc_kv_write, nc_kv_read, nc_kv_attention)
+keeps keys and values as MX blocks of E2M1 or E4M3 codes in pages.
 """
 
 import ctypes
+import math
 import struct
 from typing import Optional, Sequence
 
 import torch
 
 from . import _lib
-from ._lib import (NC_BF16, NC_E4M3, NC_E5M2, NC_EST_CURRENT, NC_EST_EMA, NC_EST_MAX_WINDOW,  # noqa: F401
+from ._lib import (NC_BF16, NC_E2M1, NC_E4M3, NC_E5M2, NC_EST_CURRENT, NC_EST_EMA, NC_EST_MAX_WINDOW,  # noqa: F401
                    NC_EST_MOST_RECENT, NC_F32, NC_MX_CEIL, NC_MX_OCP, NC_MX_PLUS1, NC_W_BF16, NC_W_FP16,
-                   NcPolicy, NcSwampPolicy, NcTensor, NcUpdateTensor)
+                   NcKvAttn, NcKvCache, NcKvRows, NcPolicy, NcSwampPolicy, NcTensor, NcUpdateTensor)
 
 COUNT_FIELDS = ("n_finite", "n_clip", "n_underflow", "n_nonfinite")
 STAT_FIELDS = ("sum_e", "sum_abs_e", "sum_e2", "sum_dir_e", "sum_xe", "sum_x2")
@@ -401,3 +405,196 @@ def nc_swamp_window(pol: NcSwampPolicy, st: torch.Tensor, in_counts: torch.Tenso
     _need(in_counts, "in_counts", torch.int64, st.shape[0], 5)
     _check(_lib.load().nc_swamp_window(ctypes.byref(pol), st.shape[0], _ptr(st), _ptr(in_counts),
                                        _stream(stream)), "nc_swamp_window")
+
+
+# -- the key/value cache -------------------------------------------------------
+
+KV_FMT = {"e2m1": NC_E2M1, "e4m3": NC_E4M3}
+
+
+class KvCache:
+    """Keys and values of past tokens as MX blocks, in pages.
+
+    data is one uint8 tensor of `pages` rows, a page each; pages may be copied
+    as rows.  `page` tokens a page (a multiple of 16), `heads` key/value heads
+    of `dim` elements (64, 96, 128, 192 or 256), fmt "e2m1" or "e4m3"."""
+
+    def __init__(self, data: torch.Tensor, page: int, heads: int, dim: int, fmt: str):
+        self.page, self.heads, self.dim, self.fmt = int(page), int(heads), int(dim), fmt
+        each = kv_page_bytes(page, heads, dim, fmt)
+        if data.dtype != torch.uint8 or data.dim() != 2 or data.shape[1] != each or not data.is_contiguous():
+            raise ValueError(f"data: shape {tuple(data.shape)} of {data.dtype}, expected contiguous "
+                             f"torch.uint8 (pages, {each})")
+        self.data, self.pages, self.device = data, data.shape[0], data.device
+        if self.pages and _lib.load().nc_kv_cache_bytes(self.pages, self.page, self.heads, self.dim, KV_FMT[fmt]) == 0:
+            raise ValueError(f"{self.pages} pages: pages * page and pages * page / 16 * heads stay below 2^31")
+        # what the calls pass on; the fields above do not change afterwards
+        self.descriptor = NcKvCache(data.data_ptr() if self.pages else None, self.pages, self.page, self.heads, self.dim,
+                                    KV_FMT[fmt])
+
+
+def kv_page_bytes(page: int, heads: int, dim: int, fmt: str) -> int:
+    """Bytes of one page of a cache."""
+    if fmt not in KV_FMT:
+        raise ValueError(f"fmt {fmt!r}: one of {sorted(KV_FMT)}")
+    if page <= 0 or page % 16:
+        raise ValueError(f"page {page}: a positive multiple of 16")
+    if heads < 1 or dim not in (64, 96, 128, 192, 256):
+        raise ValueError(f"heads {heads}, dim {dim}: at least one head of 64, 96, 128, 192 or 256 elements")
+    each = int(_lib.load().nc_kv_cache_bytes(1, page, heads, dim, KV_FMT[fmt]))
+    if each == 0:
+        raise ValueError(f"page {page}, heads {heads}: too large")
+    return each
+
+
+def new_kv_cache(pages: int, page: int, heads: int, dim: int, fmt: str = "e2m1", device="cuda") -> KvCache:
+    """A cache of `pages` pages, every token zero."""
+    return KvCache(torch.zeros((pages, kv_page_bytes(page, heads, dim, fmt)), dtype=torch.uint8, device=device), page,
+                   heads, dim, fmt)
+
+
+_KV_DTYPE = {torch.float32: (NC_F32, 4), torch.bfloat16: (NC_BF16, 8)}     # code, elements of 16 bytes
+
+
+def _rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, unit: int, dev: torch.device):
+    """Token and head stride of [tokens, heads, dim] rows: any that are multiples of 16 bytes, elements adjacent."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the cache is on {dev}")
+    ts, hs, one = t.stride()
+    if shape[0] <= 1:
+        ts = 0
+    if one != 1 or (ts | hs) & (unit - 1) or t.data_ptr() & 15:
+        raise ValueError(f"{name}: strides {t.stride()}: rows of adjacent elements that start on 16 bytes expected")
+    return ts, hs
+
+
+def _spread(t: torch.Tensor, name: str):
+    """Raise ValueError where an output's rows share memory."""
+    if t.is_contiguous():
+        return
+    at = 0
+    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1), key=lambda x: x[1]):
+        if stride <= at:
+            raise ValueError(f"{name}: strides {t.stride()}: its rows overlap")
+        at += (size - 1) * stride
+
+
+def _kv_stream(stream, dev: torch.device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _kv_tokens(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
+    """Checks of a write or read; the call's arguments from the cache to the slots."""
+    if k.dtype not in _KV_DTYPE:
+        raise TypeError(f"dtype {k.dtype} (float32 or bfloat16 expected)")
+    code, unit = _KV_DTYPE[k.dtype]
+    dev = cache.device
+    if slots.dim() != 1 or slots.device != dev:
+        raise ValueError(f"slots: shape {tuple(slots.shape)} on {slots.device}, expected one entry a token on {dev}")
+    tokens = slots.shape[0]
+    if slots.dtype is not torch.int64 or not slots.is_contiguous():
+        raise ValueError(f"slots: dtype {slots.dtype}, expected contiguous torch.int64")
+    shape = torch.Size((tokens, cache.heads, cache.dim))
+    ks, vs = _rows(k, "k", shape, k.dtype, unit, dev), _rows(v, "v", shape, k.dtype, unit, dev)
+    return (cache.descriptor, NcKvRows(_ptr(k), *ks), NcKvRows(_ptr(v), *vs), tokens, code, _ptr(slots))
+
+
+def nc_kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule="ceil", stream=None):
+    """Quantise keys and values [tokens, heads, dim] into the cache at `slots`
+    (int64, page * cache.page + offset; distinct; -1 skips a token).  k and v
+    may be slices of a fused projection."""
+    r = MX_RULE[rule] if isinstance(rule, str) else rule
+    args = _kv_tokens(cache, k, v, slots)
+    _check(_lib.load().nc_kv_write(*args, r, _kv_stream(stream, cache.device)), "nc_kv_write")
+
+
+def nc_kv_read(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
+    """The keys and values at `slots`, as fp32 or bf16 [tokens, heads, dim]."""
+    _spread(k_out, "k")
+    _spread(v_out, "v")
+    args = _kv_tokens(cache, k_out, v_out, slots)
+    _check(_lib.load().nc_kv_read(*args, _kv_stream(stream, cache.device)), "nc_kv_read")
+
+
+def kv_workspace_bytes(cache: KvCache, q: torch.Tensor, batch: int, max_q: int, max_kv: int) -> int:
+    return int(_lib.load().nc_kv_workspace_bytes(cache.descriptor, _dtype_code(q), q.shape[1], batch, max_q, max_kv))
+
+
+def new_kv_workspace(cache: KvCache, q: torch.Tensor, batch: int, max_q: int, max_kv: int) -> torch.Tensor:
+    """Device workspace for nc_kv_attention at these sizes or smaller max_q and
+    window; calls that run concurrently need workspaces of their own."""
+    return torch.empty(max(kv_workspace_bytes(cache, q, batch, max_q, max_kv), 16), dtype=torch.uint8,
+                       device=cache.device)
+
+
+def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                    table: torch.Tensor, max_q: int, max_kv: int, causal: bool = True, window: int = 0,
+                    scale: Optional[float] = None, lse: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None, stream=None):
+    """Attention of queries q [rows, q_heads, dim] over the cache, into out (as q).
+
+    Sequence b has the rows q_start[b] .. q_start[b + 1] - 1 of q (int32,
+    batch + 1) and kv_len[b] cached tokens (int32) on the pages table[b] (int32
+    [batch, pages]).  max_q and max_kv bound both on the host.  causal: the
+    queries are the sequence's last tokens; else each sees the whole cache
+    (cross attention).  window: tokens that a query sees at most, 0 for all.
+    scale: 1 / sqrt(dim) where None.  lse (fp32 [rows, q_heads]) receives
+    log sum exp of the scores; a query that sees nothing gets out 0, lse -inf."""
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"q: dtype {q.dtype} (float32 or bfloat16 expected)")
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected (rows, q_heads, {cache.dim})")
+    rows, q_heads, _ = q.shape
+    dev = cache.device
+    if q_heads == 0 or q_heads % cache.heads:
+        raise ValueError(f"q: {q_heads} heads, a multiple of the cache's {cache.heads} expected")
+    code, unit = _KV_DTYPE[q.dtype]
+    shape = torch.Size((rows, q_heads, cache.dim))
+    qs, os = _rows(q, "q", shape, q.dtype, unit, dev), _rows(out, "out", shape, q.dtype, unit, dev)
+    _spread(out, "out")
+    batch = kv_len.numel()
+    for t, name, n in ((q_start, "q_start", batch + 1), (kv_len, "kv_len", batch)):
+        if t.dtype is not torch.int32 or t.shape != (n,) or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: shape {tuple(t.shape)} of {t.dtype} on {t.device}, expected contiguous torch.int32 "
+                             f"({n},) on {dev}")
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.shape[0] != batch or not table.is_contiguous() \
+            or table.device != dev:
+        raise ValueError(f"table: shape {tuple(table.shape)} of {table.dtype} on {table.device}, expected contiguous "
+                         f"torch.int32 ({batch}, pages) on {dev}")
+    if max_q < 0 or max_kv < 0 or window < 0:
+        raise ValueError(f"max_q {max_q}, max_kv {max_kv}, window {window}: none may be negative")
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.dim)
+    if not math.isfinite(scale):
+        raise ValueError(f"scale {scale}: a finite number expected")
+    lts = 0
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != shape[:2] or lse.device != dev \
+                or (q_heads > 1 and lse.stride(1) != 1):
+            raise ValueError(f"lse: shape {tuple(lse.shape)} of {lse.dtype} on {lse.device}, expected torch.float32 "
+                             f"({rows}, {q_heads}) on {dev}, heads adjacent")
+        _spread(lse, "lse")
+        lts = lse.stride(0) if rows > 1 else 0
+    _need(ws, "ws", torch.uint8, 0)
+    if rows == 0 or batch == 0 or max_q == 0:
+        return
+    c = cache.descriptor
+    lib = _lib.load()
+    if ws is None:
+        need = int(lib.nc_kv_workspace_bytes(c, code, q_heads, batch, max_q, max_kv))
+        if need:
+            # on the call's own stream: freed memory is handed out again in that stream's order
+            on = torch.cuda.current_stream(dev) if stream is None else (
+                stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev))
+            with torch.cuda.stream(on):
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    a = NcKvAttn(_ptr(q), *qs, _ptr(out), *os, _ptr(lse), lts, _ptr(q_start), _ptr(kv_len), _ptr(table), table.shape[1],
+                 batch, rows, q_heads, max_q, max_kv, 1 if causal else 0, window, scale)
+    _check(lib.nc_kv_attention(c, a, code, _ptr(ws), 0 if ws is None else ws.numel(), _kv_stream(stream, dev)),
+           "nc_kv_attention")

@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(PKG, "libnarrowcast.so")
 NC_OK, NC_E_ARG, NC_E_ALIGN, NC_E_SHAPE, NC_E_UNSUPPORTED, NC_E_HIP, NC_E_WORKSPACE, NC_E_SCRATCH = range(8)
 NC_STATIC_SCRATCH_BYTES = 8 << 20
 NC_F32, NC_BF16 = 0, 1
-NC_E4M3, NC_E5M2 = 0, 1
+NC_E4M3, NC_E5M2, NC_E2M1 = 0, 1, 2
 NC_MX_OCP, NC_MX_PLUS1, NC_MX_CEIL = 0, 1, 2
 NC_EST_CURRENT, NC_EST_MOST_RECENT, NC_EST_MAX_WINDOW, NC_EST_EMA = 0, 1, 2, 3
 NC_MX_ROWS, NC_MX_COLS = 0, 1
@@ -65,11 +65,30 @@ class NcSwampState(ctypes.Structure):
     _fields_ = [(n, c_int32) for n in ("run", "promoted", "steps", "reserved")]
 
 
+class NcKvCache(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("pages", c_int64), ("page", c_int32), ("heads", c_int32), ("dim", c_int32),
+                ("fmt", c_int32)]
+
+
+class NcKvRows(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("token_stride", c_int64), ("head_stride", c_int64)]
+
+
+class NcKvAttn(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("q_token_stride", c_int64), ("q_head_stride", c_int64),
+                ("out", c_void_p), ("out_token_stride", c_int64), ("out_head_stride", c_int64),
+                ("lse", c_void_p), ("lse_token_stride", c_int64),
+                ("q_start", c_void_p), ("kv_len", c_void_p), ("table", c_void_p)] + \
+               [(n, c_int32) for n in ("table_pages", "batch", "total_q", "q_heads", "max_q", "max_kv", "causal",
+                                       "window")] + [("scale", ctypes.c_float)]
+
+
 NC_W_BF16, NC_W_FP16 = 0, 1
 
 EXPORTS = ("nc_amax", "nc_scale_update", "nc_cast_tensor", "nc_cast_tensor_static", "nc_cast_tensor_sr", "nc_cast_mx", "nc_dequant",
            "nc_cast_stats", "nc_workspace_bytes", "nc_status_string", "nc_swamp_workspace_bytes",
-           "nc_swamp_watch", "nc_swamp_window")
+           "nc_swamp_watch", "nc_swamp_window", "nc_kv_cache_bytes", "nc_kv_write", "nc_kv_read", "nc_kv_attention",
+           "nc_kv_workspace_bytes")
 
 _lib = None
 
@@ -102,12 +121,20 @@ def load():
     lib.nc_swamp_workspace_bytes.restype = c_size_t
     lib.nc_swamp_watch.argtypes = [U, c_int32, c_int32, c_void_p, c_void_p, c_size_t, c_void_p]
     lib.nc_swamp_window.argtypes = [POINTER(NcSwampPolicy), c_int32, c_void_p, c_void_p, c_void_p]
+    C, V = POINTER(NcKvCache), POINTER(NcKvRows)
+    lib.nc_kv_cache_bytes.argtypes = [c_int64, c_int32, c_int32, c_int32, c_int32]
+    lib.nc_kv_cache_bytes.restype = c_size_t
+    lib.nc_kv_write.argtypes = [C, V, V, c_int64, c_int32, c_void_p, c_int32, c_void_p]
+    lib.nc_kv_read.argtypes = [C, V, V, c_int64, c_int32, c_void_p, c_void_p]
+    lib.nc_kv_attention.argtypes = [C, POINTER(NcKvAttn), c_int32, c_void_p, c_size_t, c_void_p]
+    lib.nc_kv_workspace_bytes.argtypes = [C, c_int32, c_int32, c_int32, c_int32, c_int32]
+    lib.nc_kv_workspace_bytes.restype = c_size_t
     lib.nc_workspace_bytes.argtypes = [T, c_int32]
     lib.nc_workspace_bytes.restype = c_size_t
     lib.nc_status_string.argtypes = [c_int32]
     lib.nc_status_string.restype = c_char_p
     for name in ("nc_amax", "nc_scale_update", "nc_cast_tensor", "nc_cast_tensor_static", "nc_cast_tensor_sr", "nc_cast_mx", "nc_dequant",
-                 "nc_cast_stats", "nc_swamp_watch", "nc_swamp_window"):
+                 "nc_cast_stats", "nc_swamp_watch", "nc_swamp_window", "nc_kv_write", "nc_kv_read", "nc_kv_attention"):
         getattr(lib, name).restype = c_int32
     _lib = lib
     return lib

@@ -1,0 +1,143 @@
+// The paged key/value cache: layout, converts and the launch interface shared
+// by the kernels that write, read and attend over it.
+//
+// A token's key row and value row of one head are MX blocks: 32 consecutive
+// elements share a power of two 2^X (byte X + 127) and are codes of E2M1
+// (4 bits) or E4M3 (8 bits).  One byte buffer holds it all:
+//
+//   page p, head h, tile t of the page (16 tokens):
+//     base = ((p * heads + h) * page / 16 + t) * kTile
+//     key codes [16 R] | value codes [16 R] | key scales [nb][16] | value scales [nb][16]
+//
+// with R = dim * bits / 8 the bytes of a row and nb = dim / 32.  A head's
+// page is one contiguous run, a tile is what one wave reads with one load per
+// 16 bytes of row, and the orders inside a tile are those of the matrix
+// instructions, so attention moves codes from memory to operands without a
+// shuffle.  A row's bytes are cut into segments of 64, 32 and 16 bytes (w):
+//
+//   keys:   [segment][piece g = 0..3][token 0..15][w / 4 bytes]
+//           a lane (token, g) reads w / 4 contiguous bytes of its own token:
+//           the k index of the operand that has keys as its rows
+//   values: [segment][quad of tokens 0..3][c = 0..15][token of the quad][w / 16 bytes]
+//           a lane (quad, c) reads four tokens of the same few elements: the
+//           k index of the product with the weights runs over tokens
+//
+// No byte is shared by two tokens, so tokens are written independently.
+#pragma once
+
+#include "nc_device.h"
+
+namespace nc {
+
+constexpr int kKvTokens = 16;   // tokens of a tile
+
+template <int FMT, int D> struct Kv {
+  static constexpr int BITS = FMT == NC_E2M1 ? 4 : 8;
+  static constexpr int DPB = 8 / BITS;              // elements of a byte
+  static constexpr int R = D * BITS / 8;            // bytes of a row
+  static constexpr int NB = D / 32;                 // blocks of a row
+  static constexpr int TILE = 32 * (R + NB);        // bytes of a tile
+  static constexpr int KC = 0, VC = 16 * R, KS = 32 * R, VS = 32 * R + 16 * NB;
+  static constexpr int N4 = R / 64, N2 = (R % 64) / 32, N1 = (R % 32) / 16;
+  static constexpr int NSEG = N4 + N2 + N1;
+  static constexpr int DW = R / 16;                 // dwords of codes per lane and tile (keys, and values)
+  static constexpr int w(int s) { return s < N4 ? 64 : (s < N4 + N2 ? 32 : 16); }
+  static constexpr int off(int s) { return s <= N4 ? 64 * s : (s <= N4 + N2 ? 64 * N4 + 32 * (s - N4) : R); }
+  static constexpr int dim0(int s) { return off(s) * DPB; }
+  static constexpr int piece(int s) { return w(s) / 4 * DPB; }   // elements of a key piece
+  static constexpr int lane(int s) { return w(s) / 16 * DPB; }   // elements of a value lane and token
+};
+
+// Bytes of a tile for run-time sizes (host).
+inline int64_t kv_tile_bytes(int fmt, int dim) { return 32 * (int64_t)(dim * (fmt == NC_E2M1 ? 4 : 8) / 8 + dim / 32); }
+
+// gfx950's scaled converts, codes -> two bf16 (exact: a code has at most four
+// significant bits; below bf16's range the result is rounded to nearest even).
+// scale: 2^X as a float whose exponent field is the scale byte (0 stands for
+// 2^-127, 255 gives NaN: measured for every code and scale byte).
+__device__ __forceinline__ float kv_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Codes 2i, 2i + 1 of a dword (E2M1: byte i; E4M3: half i) -> packed bf16.
+template <int FMT>
+__device__ __forceinline__ uint32_t kv_pair(uint32_t codes, float scale, int i) {
+  bf16x2_t r;
+  if constexpr (FMT == NC_E2M1) {
+    switch (i) {
+      case 0: r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0); break;
+      case 1: r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1); break;
+      case 2: r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2); break;
+      default: r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3); break;
+    }
+  } else {
+    if (i == 0) r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false);
+    else r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, true);
+  }
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// What a cache and a view of rows are to the kernels.
+struct KvCache {
+  uint8_t* data;
+  int64_t slots;        // pages * page
+  int32_t page;         // tokens of a page, a multiple of 16
+  int32_t heads;
+};
+template <typename P> struct KvRows {   // element (token, head, i) at p[token * ts + head * hs + i]
+  P p;
+  int64_t ts, hs;
+};
+
+// One attention call (kernel argument).
+struct KvAttn {
+  KvCache cache;
+  KvRows<const void*> q;
+  KvRows<void*> out;
+  float* lse;              // [total_q][lse_ts], nullable
+  int64_t lse_ts;
+  const int32_t* q_start;  // [batch + 1]
+  const int32_t* kv_len;   // [batch]
+  const int32_t* table;    // [batch][table_w] page numbers
+  int32_t table_w, batch, total_q, max_q, max_kv;
+  int32_t group;           // query heads of a cache head
+  int32_t causal, window;  // window 0: none
+  float scale2;            // score scale times log2(e)
+  // the split: each workgroup takes `rows` rows (query, head of the group) of
+  // one sequence and cache head and `chunk` tiles of keys
+  int32_t row_groups, chunk, chunks;
+  float* part;             // partial results, chunks > 1 only
+};
+
+// What the split of a call is, from its sizes (host): shared by the workspace
+// size and the launch.
+struct KvPlan {
+  int32_t rows;         // rows of a workgroup
+  int32_t waves;        // waves of a workgroup
+  int32_t row_groups;   // workgroups along the rows of one (sequence, head)
+  int32_t chunk;        // tiles of 16 keys of a workgroup
+  int32_t chunks;       // workgroups along the keys, at most `most`
+  int32_t most;         // does not fall as the span of keys grows
+};
+
+constexpr int kKvFewWaves = 4;
+// Most rows of a workgroup of the few-row kernel: 64 where queries, sums and a
+// step's codes fit the registers of two waves a SIMD or one, else 32.
+constexpr int kv_few_rows_most(int dtype, int dim) { return dtype == NC_BF16 && dim <= 128 ? 64 : 32; }
+
+// Rows (query i of the sequence, head j of the group) are numbered i * group + j.
+// Partial results of chunk c, sequence b, head h, row r: D unnormalised sums, at
+// ((b * heads + h) * chunks + c) * rows_all + r, then the running maximum and sum.
+inline size_t kv_part_bytes(int64_t batch, int64_t heads, int64_t chunks, int64_t rows_all, int dim) {
+  return chunks > 1 ? (size_t)(batch * heads * chunks * rows_all) * (size_t)(dim + 2) * 4 : 0;
+}
+
+hipError_t launch_kv_write(const KvCache& c, int fmt, int dim, const KvRows<const void*>& k, const KvRows<const void*>& v,
+                           int dtype, const int64_t* slots, int64_t tokens, int rule, hipStream_t stream);
+hipError_t launch_kv_read(const KvCache& c, int fmt, int dim, const KvRows<void*>& k, const KvRows<void*>& v, int dtype,
+                          const int64_t* slots, int64_t tokens, hipStream_t stream);
+hipError_t kv_few_e2m1_bf16(const KvAttn& a, int dim, const KvPlan& p, hipStream_t stream);
+hipError_t kv_few_e2m1_f32(const KvAttn& a, int dim, const KvPlan& p, hipStream_t stream);
+hipError_t kv_few_e4m3_bf16(const KvAttn& a, int dim, const KvPlan& p, hipStream_t stream);
+hipError_t kv_few_e4m3_f32(const KvAttn& a, int dim, const KvPlan& p, hipStream_t stream);
+hipError_t launch_kv_join(const KvAttn& a, int dim, int dtype, hipStream_t stream);
+
+}  // namespace nc

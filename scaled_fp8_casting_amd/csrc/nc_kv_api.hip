@@ -1,0 +1,174 @@
+// The C-ABI of the key/value cache: argument checks, the split of attention
+// over workgroups, launches.  No allocation, no state.
+#include <algorithm>
+#include <cmath>
+
+#include "nc_kv.h"
+
+using namespace nc;
+
+namespace {
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool valid_dim(int32_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
+
+// fmt, dim and page, then sizes: slots and tiles are numbered in 31 bits.
+nc_status check_cache(const nc_kv_cache* c, bool data) {
+  if (c == nullptr) return NC_E_ARG;
+  if ((c->fmt != NC_E2M1 && c->fmt != NC_E4M3) || !valid_dim(c->dim)) return NC_E_UNSUPPORTED;
+  if (c->page <= 0 || c->page % kKvTokens != 0) return NC_E_SHAPE;
+  if (c->pages < 0 || c->heads < 1) return NC_E_ARG;
+  const int64_t most = INT32_MAX;
+  if (c->heads > 65536 || c->pages > most / c->page || c->pages * (c->page / kKvTokens) > most / c->heads) return NC_E_ARG;
+  if (!data || c->pages == 0) return NC_OK;
+  if (c->data == nullptr) return NC_E_ARG;
+  return aligned16(c->data) ? NC_OK : NC_E_ALIGN;
+}
+
+// 16-byte pieces of rows: pointer and strides.
+nc_status check_rows(const void* p, int64_t ts, int64_t hs, nc_dtype dt) {
+  const int64_t unit = dt == NC_BF16 ? 8 : 4;
+  if (p == nullptr || ts < 0 || hs < 0) return NC_E_ARG;
+  return aligned16(p) && ts % unit == 0 && hs % unit == 0 ? NC_OK : NC_E_ALIGN;
+}
+
+KvCache cache_of(const nc_kv_cache* c) { return KvCache{c->data, c->pages * c->page, c->page, c->heads}; }
+nc_status hip_status(hipError_t e) { return e == hipSuccess ? NC_OK : NC_E_HIP; }
+
+nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_rows* v, int64_t tokens, nc_dtype dtype,
+                       const int64_t* slots) {
+  nc_status s = check_cache(c, true);
+  if (s != NC_OK) return s;
+  if (dtype != NC_F32 && dtype != NC_BF16) return NC_E_UNSUPPORTED;
+  // one lane per eight elements, numbered in 32 bits
+  if (tokens < 0 || tokens > ((int64_t)1 << 31) || (tokens + 4) * c->heads > ((int64_t)1 << 32) / (c->dim / 8) - 256)
+    return NC_E_ARG;
+  if (tokens == 0) return NC_OK;
+  if (k == nullptr || v == nullptr || slots == nullptr) return NC_E_ARG;
+  if (((uintptr_t)slots & 7u) != 0) return NC_E_ALIGN;
+  if ((s = check_rows(k->data, k->token_stride, k->head_stride, dtype)) != NC_OK) return s;
+  return check_rows(v->data, v->token_stride, v->head_stride, dtype);
+}
+
+// The split of a call.  span: tiles of 16 keys that a row group may reach.
+KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_t rows_all, int64_t span) {
+  KvPlan p;
+  p.waves = kKvFewWaves;
+  const int most = kv_few_rows_most(dtype, dim);
+  p.rows = rows_all <= 16 ? 16 : (rows_all <= 32 || most == 32 ? 32 : 64);
+  p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
+  const int64_t base = std::max<int64_t>(1, batch * heads * p.row_groups);
+  // at least 32 tiles (512 keys) each, at most about 1024 workgroups
+  const int64_t want = std::min<int64_t>((1024 + base - 1) / base, span / 32);
+  const int64_t chunks = std::max<int64_t>(1, want);
+  p.most = (int32_t)chunks;
+  p.chunk = (int32_t)std::max<int64_t>(1, (span + chunks - 1) / chunks);
+  p.chunks = (int32_t)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
+  return p;
+}
+
+int64_t span_of(int64_t max_kv, int64_t max_q, int64_t window) {
+  const int64_t keys = window > 0 ? std::min<int64_t>(max_kv, window + max_q) : max_kv;
+  return (keys + kKvTokens - 1) / kKvTokens + (window > 0 ? 1 : 0);
+}
+
+nc_status check_sizes(const nc_kv_cache* c, int32_t q_heads, int32_t batch, int32_t max_q, int32_t max_kv) {
+  if (batch < 0 || max_q < 0 || max_kv < 0 || q_heads < 1) return NC_E_ARG;
+  if (q_heads % c->heads != 0) return NC_E_SHAPE;
+  // rows of a sequence and head, and of all, are numbered in 31 bits
+  if ((int64_t)max_q * (q_heads / c->heads) > INT32_MAX / 2) return NC_E_ARG;
+  if ((int64_t)batch * c->heads > INT32_MAX / std::max<int64_t>(1, (int64_t)max_q * (q_heads / c->heads))) return NC_E_ARG;
+  return NC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nc_kv_cache_bytes(int64_t pages, int32_t page, int32_t heads, int32_t dim, int32_t fmt) {
+  const nc_kv_cache c = {nullptr, pages, page, heads, dim, fmt};
+  if (check_cache(&c, false) != NC_OK) return 0;
+  return (size_t)(pages * (page / kKvTokens) * heads * kv_tile_bytes(fmt, dim));
+}
+
+nc_status nc_kv_write(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_rows* v, int64_t tokens, nc_dtype dtype,
+                      const int64_t* slots, nc_mx_rule rule, void* stream) {
+  if (rule != NC_MX_OCP && rule != NC_MX_PLUS1 && rule != NC_MX_CEIL) return NC_E_UNSUPPORTED;
+  const nc_status s = check_tokens(c, k, v, tokens, dtype, slots);
+  if (s != NC_OK || tokens == 0) return s;
+  return hip_status(launch_kv_write(cache_of(c), c->fmt, c->dim, {k->data, k->token_stride, k->head_stride},
+                                    {v->data, v->token_stride, v->head_stride}, dtype, slots, tokens, rule,
+                                    (hipStream_t)stream));
+}
+
+nc_status nc_kv_read(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_rows* v, int64_t tokens, nc_dtype dtype,
+                     const int64_t* slots, void* stream) {
+  const nc_status s = check_tokens(c, k, v, tokens, dtype, slots);
+  if (s != NC_OK || tokens == 0) return s;
+  return hip_status(launch_kv_read(cache_of(c), c->fmt, c->dim, {k->data, k->token_stride, k->head_stride},
+                                   {v->data, v->token_stride, v->head_stride}, dtype, slots, tokens, (hipStream_t)stream));
+}
+
+size_t nc_kv_workspace_bytes(const nc_kv_cache* c, nc_dtype dtype, int32_t q_heads, int32_t batch, int32_t max_q,
+                             int32_t max_kv) {
+  if (check_cache(c, false) != NC_OK || (dtype != NC_F32 && dtype != NC_BF16)) return 0;
+  if (check_sizes(c, q_heads, batch, max_q, max_kv) != NC_OK || batch == 0 || max_q == 0) return 0;
+  const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
+  // a window only shortens the span, and a shorter span never raises the most
+  const KvPlan p = plan_of(c->dim, dtype, batch, c->heads, rows, span_of(max_kv, max_q, 0) + 1);
+  return kv_part_bytes(batch, c->heads, p.most, rows, c->dim);
+}
+
+nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dtype, void* ws, size_t ws_bytes,
+                          void* stream) {
+  nc_status s = check_cache(c, true);
+  if (s != NC_OK) return s;
+  if (dtype != NC_F32 && dtype != NC_BF16) return NC_E_UNSUPPORTED;
+  if (a == nullptr) return NC_E_ARG;
+  if ((s = check_sizes(c, a->q_heads, a->batch, a->max_q, a->max_kv)) != NC_OK) return s;
+  if (a->total_q < 0 || a->table_pages < 0 || a->window < 0 || !std::isfinite(a->scale)) return NC_E_ARG;
+  if (a->batch == 0 || a->max_q == 0 || a->total_q == 0) return NC_OK;
+  if (a->q_start == nullptr || a->kv_len == nullptr || (a->table == nullptr && a->table_pages > 0)) return NC_E_ARG;
+  if ((s = check_rows(a->q, a->q_token_stride, a->q_head_stride, dtype)) != NC_OK) return s;
+  if ((s = check_rows(a->out, a->out_token_stride, a->out_head_stride, dtype)) != NC_OK) return s;
+  if (a->lse_token_stride < 0) return NC_E_ARG;
+  if ((((uintptr_t)a->q_start | (uintptr_t)a->kv_len | (uintptr_t)a->table | (uintptr_t)a->lse) & 3u) != 0) return NC_E_ALIGN;
+
+  KvAttn k = {};
+  k.cache = cache_of(c);
+  k.q = {a->q, a->q_token_stride, a->q_head_stride};
+  k.out = {a->out, a->out_token_stride, a->out_head_stride};
+  k.lse = a->lse;
+  k.lse_ts = a->lse_token_stride;
+  k.q_start = a->q_start;
+  k.kv_len = a->kv_len;
+  k.table = a->table;
+  k.table_w = c->pages > 0 ? a->table_pages : 0;
+  k.batch = a->batch;
+  k.total_q = a->total_q;
+  k.max_q = a->max_q;
+  k.max_kv = a->max_kv;
+  k.group = a->q_heads / c->heads;
+  k.causal = a->causal != 0;
+  k.window = a->window;
+  k.scale2 = a->scale * 1.4426950408889634f;
+  const int64_t rows = (int64_t)a->max_q * k.group;
+  const KvPlan p = plan_of(c->dim, dtype, a->batch, c->heads, rows, span_of(a->max_kv, a->max_q, a->window));
+  k.row_groups = p.row_groups;
+  k.chunk = p.chunk;
+  k.chunks = p.chunks;
+  k.part = (float*)ws;
+  if ((int64_t)a->batch * c->heads * p.row_groups * p.chunks > INT32_MAX) return NC_E_ARG;
+  if (p.chunks > 1) {
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < kv_part_bytes(a->batch, c->heads, p.chunks, rows, c->dim))
+      return NC_E_WORKSPACE;
+  }
+  const hipStream_t st = (hipStream_t)stream;
+  hipError_t e;
+  if (c->fmt == NC_E2M1) e = dtype == NC_BF16 ? kv_few_e2m1_bf16(k, c->dim, p, st) : kv_few_e2m1_f32(k, c->dim, p, st);
+  else e = dtype == NC_BF16 ? kv_few_e4m3_bf16(k, c->dim, p, st) : kv_few_e4m3_f32(k, c->dim, p, st);
+  if (e == hipSuccess && p.chunks > 1) e = launch_kv_join(k, c->dim, dtype, st);
+  return hip_status(e);
+}
+
+}  // extern "C"

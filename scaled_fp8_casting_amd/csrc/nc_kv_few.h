@@ -1,0 +1,550 @@
+// Attention over the paged cache for few rows: the next tokens of running
+// sequences.
+//
+// Row r = (query i, head j of the group) of a sequence and a cache head; key
+// t is seen when start(i) <= t < end(i).  With s = scale log2(e) q.k, m the
+// running maximum of a row and l the running sum of 2^(s - m),
+//   out = (sum_t 2^(s_t - m) v_t) / l,   lse = (m + log2 l) ln 2,
+// in one pass over the cache: a new maximum m' multiplies what is there by
+// 2^(m - m').  A row that sees nothing has l = 0: out = 0, lse = -inf.
+//
+// What bounds it is the cache's bytes, so nothing but registers lies between
+// memory and the matrix instructions.  A wave takes 16 NT rows and runs over
+// tiles of 16 tokens:
+//
+//   S^T = K Q^T   16x16x32 bf16: lane (key m, group g of k) loads its own key's
+//                 codes (one load per tile and segment), converts them with
+//                 their block's scale to bf16 -- exactly, a code has at most 4
+//                 significant bits -- and multiplies
+//   softmax       a lane has query n = lane % 16 and keys 4 g + i, so maximum and
+//                 sum run over registers, then over the four groups
+//   O^T = V^T P^T the weights are in place as operand: k index 8 g + e stands for
+//                 key 4 g + e of the first tile (e < 4) or the second; the lane
+//                 (m, g) loads quad g of both value tiles
+//
+// fp32 queries and weights are cut into three bf16 parts of 8 significant bits,
+// exactly; products and sums are fp32.  bf16 calls round the weights to bf16
+// (2^-8 relative, as their output is) and sum them before the rounding.
+//
+// The waves of a workgroup take turns along the keys, the workgroups of a
+// (sequence, head) take chunks of them; sums meet in LDS and, across
+// workgroups, in a second kernel.
+#pragma once
+
+#include "nc_kv.h"
+
+namespace nc {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ f32x4_t mfma16(const u32x4& a, const u32x4& b, const f32x4_t& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Maximum and sum over the lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float max_groups(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float add_groups(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Two floats -> packed bf16, nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
+
+// The keys of one sequence that a workgroup's rows see.
+struct KvSpan {
+  int n, q_len, q0;        // cached tokens, queries, first query's row in q
+};
+__device__ __forceinline__ KvSpan kv_span(const KvAttn& a, int b) {
+  KvSpan s;
+  const int64_t held = (int64_t)a.table_w * a.cache.page;
+  int n = a.kv_len[b];
+  n = min(max(n, 0), a.max_kv);
+  s.n = held < n ? (int)held : n;
+  // offsets outside q give an empty sequence, never an access outside q
+  const int q0 = a.q_start[b], q1 = a.q_start[b + 1];
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.total_q;
+  s.q0 = ok ? q0 : 0;
+  s.q_len = ok ? min(q1 - q0, a.max_q) : 0;
+  return s;
+}
+// Query i sees keys [kv_start, kv_end).
+__device__ __forceinline__ int kv_end(const KvAttn& a, const KvSpan& s, int i) {
+  return a.causal ? min(s.n, s.n - s.q_len + 1 + i) : s.n;
+}
+__device__ __forceinline__ int kv_begin(const KvAttn& a, int end) { return a.window ? max(0, end - a.window) : 0; }
+
+// The number of the tile (page, head, tile of the page) that holds tokens
+// [16 t, 16 t + 16) of sequence b, or -1 for a page outside the cache.
+__device__ __forceinline__ int kv_tile_at(const KvAttn& a, int b, int h, int t) {
+  const uint32_t per = (uint32_t)a.cache.page / kKvTokens;
+  const uint32_t pg = (uint32_t)t / per;
+  if (pg >= (uint32_t)a.table_w) return -1;
+  const int32_t id = a.table[(int64_t)b * a.table_w + pg];
+  if (id < 0 || (int64_t)id * a.cache.page >= a.cache.slots) return -1;
+  return (int)(((uint32_t)id * (uint32_t)a.cache.heads + (uint32_t)h) * per + ((uint32_t)t - pg * per));
+}
+
+// Four elements of a row's result, from its sums.
+template <int DT>
+__device__ __forceinline__ void kv_result(const KvAttn& a, const KvSpan& sp, int h, int r, int c, const f32x4_t& o, float top,
+                                          float sum) {
+  const int i = r / a.group, head = h * a.group + r - i * a.group;
+  const int64_t row = sp.q0 + i;
+  const float x = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t at = row * a.out.ts + head * a.out.hs + c;
+  if constexpr (DT == NC_BF16)
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out.p) + at) =
+        u32x2{pack_bf16(o[0] * x, o[1] * x), pack_bf16(o[2] * x, o[3] * x)};
+  else
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out.p) + at) = o * x;
+  if (a.lse != nullptr && c == 0) a.lse[row * a.lse_ts + head] = (top + log2f(sum)) * kLn2;
+}
+
+template <int FMT, int D> struct KvRegs {      // one tile's codes and scales in a lane
+  using L = Kv<FMT, D>;
+  uint32_t k[L::DW], v[L::DW];
+  uint32_t ks[L::NSEG], vs[L::NSEG];
+};
+
+template <int N>
+__device__ __forceinline__ void load_dwords(uint32_t* r, const uint8_t* p) {
+  if constexpr (N == 4) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = v[i];
+  } else if constexpr (N == 2) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    r[0] = v.x;
+    r[1] = v.y;
+  } else {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+template <int FMT, int D, int S = 0>
+__device__ __forceinline__ void load_tile(KvRegs<FMT, D>& r, const uint8_t* t, int m, int g) {
+  using L = Kv<FMT, D>;
+  if constexpr (S < L::NSEG) {
+    constexpr int w = L::w(S), off = L::off(S), n = w / 16;
+    load_dwords<n>(r.k + off / 16, t + L::KC + 16 * off + (g * 16 + m) * (w / 4));
+    load_dwords<n>(r.v + off / 16, t + L::VC + 16 * off + (g * 16 + m) * (w / 4));
+    r.ks[S] = t[L::KS + ((L::dim0(S) + g * L::piece(S)) / 32) * 16 + m];
+    r.vs[S] = *reinterpret_cast<const uint32_t*>(t + L::VS + ((L::dim0(S) + m * L::lane(S)) / 32) * 16 + 4 * g);
+    load_tile<FMT, D, S + 1>(r, t, m, g);
+  }
+}
+
+// A float as three bf16 numbers, in the high halves: 8 significant bits are cut
+// off at a time, so every part and remainder is exact.
+__device__ __forceinline__ void cut(uint32_t x, uint32_t (&part)[3]) {
+  part[0] = x;
+  part[1] = __float_as_uint(__uint_as_float(x) - __uint_as_float(x & 0xFFFF0000u));
+  part[2] = __float_as_uint(__uint_as_float(part[1]) - __uint_as_float(part[1] & 0xFFFF0000u));
+}
+
+// Queries as operands: rows of 16 lanes n, k step j of a segment: the eight
+// elements that a key piece has there.
+template <int DT> struct QParts { static constexpr int N = DT == NC_BF16 ? 1 : 3; };
+template <int DT>
+__device__ __forceinline__ void load_q(u32x4* q, const void* p, int64_t at, bool live) {
+  if constexpr (DT == NC_BF16) {
+    q[0] = live ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at) : u32x4{0, 0, 0, 0};
+  } else {
+    u32x4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (live) {
+      const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + at);
+      x[0] = s[0];
+      x[1] = s[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[3], b[3];
+      cut(x[i >> 1][2 * (i & 1)], a);
+      cut(x[i >> 1][2 * (i & 1) + 1], b);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) q[c][i] = __builtin_amdgcn_perm(b[c], a[c], 0x07060302u);
+    }
+  }
+}
+
+// Halves lo (0) or hi (1) of two packed pairs.
+__device__ __forceinline__ uint32_t zip(uint32_t a, uint32_t b, int hi) {
+  return hi ? __builtin_amdgcn_perm(b, a, 0x07060302u) : __builtin_amdgcn_perm(b, a, 0x05040100u);
+}
+
+// Packed bf16: 1.0 in the halves that hold an infinity or NaN, and a mask of
+// the halves that are not zero.
+__device__ __forceinline__ uint32_t not_finite16(uint32_t x) {
+  return ((x & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
+}
+__device__ __forceinline__ uint32_t whole16(uint32_t x) {
+  return (x & 0xFFFFu ? 0xFFFFu : 0u) | (x & 0xFFFF0000u ? 0xFFFF0000u : 0u);
+}
+
+// Tiles of 16 keys that a wave takes at a time: 4 while the raw codes of a
+// step stay within 40 registers, else 2.
+template <int FMT, int D> constexpr int few_tiles() { return Kv<FMT, D>::DW <= 4 ? 4 : 2; }
+
+template <int FMT, int D, int DT, int NT> struct Few {
+  using L = Kv<FMT, D>;
+  static constexpr int QP = QParts<DT>::N;       // parts of a query
+  static constexpr int PP = QP;                  // parts of a weight
+  static constexpr int KT = few_tiles<FMT, D>();
+  static constexpr int MT = D / 16;              // output tiles of 16 elements
+
+  u32x4 q[NT][D / 32][QP];
+  f32x4_t o[NT][MT];
+  float m[NT], l[NT];                            // l: this lane's keys only
+  int end[NT], begin[NT];                        // keys that the lane's row sees
+
+  // One step of KT tiles.  base: key of the first; MASKED: some row sees some
+  // key of the step not, or a tile is missing (bit of `there` off).
+  template <bool MASKED>
+  __device__ __forceinline__ void step(const KvRegs<FMT, D> (&r)[KT], int base, uint32_t there, int n_keys, float scale2,
+                                       int g) {
+    f32x4_t s[NT][KT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < KT; ++j) s[t][j] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < KT; ++j) {
+#pragma unroll
+      for (int sg = 0; sg < L::NSEG; ++sg) {
+        const float sc = kv_scale(r[j].ks[sg]);
+        constexpr int DWS = 4 * L::BITS / 16;    // dwords of eight codes
+#pragma unroll
+        for (int st = 0; st < L::piece(sg) / 8; ++st) {
+          const uint32_t* c = r[j].k + L::off(sg) / 16 + st * DWS;
+          u32x4 a;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = kv_pair<FMT>(c[i * DWS / 4], sc, i % (4 / DWS));
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c2 = QP - 1; c2 >= 0; --c2) s[t][j] = mfma16(a, q[t][L::dim0(sg) / 32 + st][c2], s[t][j]);
+        }
+      }
+    }
+    u32x4 p[NT][KT / 2][PP];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = s[t][j][i] * scale2;
+          if constexpr (MASKED) {
+            const int key = base + 16 * j + 4 * g + i;
+            x = key < end[t] && key >= begin[t] && ((there >> j) & 1) ? x : -INFINITY;
+          }
+          s[t][j][i] = x;
+          top = fmaxf(top, x);
+        }
+      top = max_groups(top);
+      const float mn = fmaxf(m[t], top);
+      const float ref = mn == -INFINITY ? 0.0f : mn;
+      if (__ballot(mn != m[t])) {
+        const float f = exp2_fast(m[t] - ref);
+        l[t] *= f;
+#pragma unroll
+        for (int d = 0; d < MT; ++d) o[t][d] *= f;
+        m[t] = mn;
+      }
+      float sum = 0;
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = exp2_fast(s[t][j][i] - ref);
+          sum += e[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (PP == 1) {
+            p[t][j / 2][0][2 * (j & 1) + i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+          } else {
+            uint32_t x[3], y[3];
+            cut(__float_as_uint(e[2 * i]), x);
+            cut(__float_as_uint(e[2 * i + 1]), y);
+#pragma unroll
+            for (int c = 0; c < 3; ++c) p[t][j / 2][c][2 * (j & 1) + i] = __builtin_amdgcn_perm(y[c], x[c], 0x07060302u);
+          }
+        }
+      }
+      l[t] += sum;
+    }
+#pragma unroll
+    for (int a = 0; a < KT / 2; ++a) {
+      uint32_t keep[4];                          // tokens past the end hold anything: cleared
+      if constexpr (MASKED) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 2 * a + i / 2, key = base + 16 * j + 4 * g + 2 * (i & 1);
+          const bool on = (there >> j) & 1;
+          keep[i] = (on && key < n_keys ? 0xFFFFu : 0u) | (on && key + 1 < n_keys ? 0xFFFF0000u : 0u);
+        }
+      }
+#pragma unroll
+      for (int sg = 0; sg < L::NSEG; ++sg) {
+        constexpr int P4 = 2 * L::DPB;           // pairs of a dword
+        const int pairs = L::lane(sg) / 2;       // pairs of a lane and token
+        float sc[2][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[x][i] = kv_scale((r[2 * a + x].vs[sg] >> (8 * i)) & 255u);
+#pragma unroll
+        for (int pr = 0; pr < pairs; ++pr) {
+          u32x4 v[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = i * pairs + pr;     // the pair's place in the lane's codes
+              w[i] = kv_pair<FMT>(r[2 * a + x].v[L::off(sg) / 16 + at / P4], sc[x][i], at % P4);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              v[h][2 * x] = zip(w[0], w[1], h);
+              v[h][2 * x + 1] = zip(w[2], w[3], h);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int d = L::dim0(sg) / 16 + 2 * pr + h;
+            if constexpr (MASKED) {
+              u32x4 nf;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                v[h][i] &= keep[i];
+                nf[i] = not_finite16(v[h][i]);
+              }
+              // 0 times NaN is NaN: a value that is not finite must reach the rows that see it only.
+              // It counts as 0 here, and rows whose seen keys hold one get NaN.
+              if (__ballot((nf[0] | nf[1] | nf[2] | nf[3]) != 0)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[h][i] &= ~whole16(nf[i]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  u32x4 vis;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int j = 2 * a + i / 2, key = base + 16 * j + 4 * g + 2 * (i & 1);
+                    vis[i] = (key >= begin[t] && key < end[t] ? 0x3F80u : 0u) |
+                             (key + 1 >= begin[t] && key + 1 < end[t] ? 0x3F800000u : 0u);
+                  }
+                  const f32x4_t hit = mfma16(nf, vis, f32x4_t{0, 0, 0, 0});
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[t][d][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[t][d][i];
+                }
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int c = PP - 1; c >= 0; --c) o[t][d] = mfma16(v[h], p[t][a][c], o[t][d]);
+          }
+        }
+      }
+    }
+  }
+};
+
+// Four elements of a row: the call's result when the row's keys are one chunk,
+// else partial sums.  A chunk in which the row sees nothing leaves its sums
+// unwritten; its maximum says so.
+template <int DT>
+__device__ __forceinline__ void kv_store(const KvAttn& a, const KvSpan& sp, int b, int h, int chunk, int r, int rows_all,
+                                         int dim, int c, const f32x4_t& o, float top, float sum) {
+  if (a.chunks == 1) {
+    kv_result<DT>(a, sp, h, r, c, o, top, sum);
+    return;
+  }
+  const int64_t n = (int64_t)a.batch * a.cache.heads * a.chunks * rows_all;
+  const int64_t at = ((int64_t)(b * a.cache.heads + h) * a.chunks + chunk) * rows_all + r;
+  if (top != -INFINITY || sum != 0.0f) *reinterpret_cast<f32x4_t*>(a.part + at * dim + c) = o;
+  if (c == 0) {
+    float* ml = a.part + n * dim + at * 2;
+    ml[0] = top;
+    ml[1] = sum;
+  }
+}
+
+template <int FMT, int D, int DT, int NT, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) kv_few(KvAttn a) {
+  using L = Kv<FMT, D>;
+  using F = Few<FMT, D, DT, NT>;
+  constexpr int KT = F::KT;
+  // one row tile's sums of every wave, then every row's maximum and sum
+  __shared__ __align__(16) float lds[WAVES * 16 * (D + 4) + WAVES * 16 * NT * 2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  // workgroup -> chunk of keys, row group, head, sequence
+  uint32_t id = blockIdx.x;
+  const int chunk = id % a.chunks;
+  id /= a.chunks;
+  const int rg = id % a.row_groups;
+  id /= a.row_groups;
+  const int h = id % a.cache.heads, b = id / a.cache.heads;
+  const KvSpan sp = kv_span(a, b);
+  const int rows_all = a.max_q * a.group, rows = sp.q_len * a.group, row0 = rg * 16 * NT;
+  if (row0 >= rows) return;
+  const int i_lo = row0 / a.group, i_hi = (min(rows, row0 + 16 * NT) - 1) / a.group;
+  // keys that some row sees, and keys that every row sees
+  const int any_end = kv_end(a, sp, i_hi), all_end = kv_end(a, sp, i_lo);
+  const int any_begin = kv_begin(a, all_end), all_begin = kv_begin(a, any_end);
+  const int t0 = any_begin / 16 + chunk * a.chunk;
+  const int t1 = min((any_end + 15) >> 4, t0 + a.chunk);
+
+  F f;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = row0 + 16 * t + m;
+    const bool live = r < rows;
+    const int i = live ? r / a.group : 0, j = live ? r - i * a.group : 0;
+    f.end[t] = kv_end(a, sp, i);
+    f.begin[t] = kv_begin(a, f.end[t]);
+    f.m[t] = -INFINITY;
+    f.l[t] = 0;
+#pragma unroll
+    for (int d = 0; d < F::MT; ++d) f.o[t][d] = f32x4_t{0, 0, 0, 0};
+    const int64_t at = (int64_t)(sp.q0 + i) * a.q.ts + (int64_t)(h * a.group + j) * a.q.hs;
+#pragma unroll
+    for (int sg = 0; sg < L::NSEG; ++sg)
+#pragma unroll
+      for (int st = 0; st < L::piece(sg) / 8; ++st)
+        load_q<DT>(f.q[t][L::dim0(sg) / 32 + st], a.q.p, at + L::dim0(sg) + g * L::piece(sg) + 8 * st, live);
+  }
+
+  // Steps of KT tiles, the waves in turn.  Lane i looks up the i-th tile that
+  // the wave takes, 64 tiles at a time.
+  constexpr int STRIDE = KT * WAVES;
+  int ids = -1;
+  KvRegs<FMT, D> next[KT];
+  uint32_t there = 0;
+  auto look_up = [&](int k) {                    // k: the wave's next step
+    const int t = t0 + (k + lane / KT) * STRIDE + wave * KT + lane % KT;
+    ids = t < t1 ? kv_tile_at(a, b, h, t) : -1;
+  };
+  auto fetch = [&](int k) {
+    there = 0;
+#pragma unroll
+    for (int j = 0; j < KT; ++j) {
+      const int tile = __builtin_amdgcn_readlane(ids, (k % (64 / KT)) * KT + j);
+      there |= tile >= 0 ? 1u << j : 0u;
+      load_tile<FMT, D>(next[j], a.cache.data + (int64_t)max(tile, 0) * L::TILE, m, g);
+    }
+  };
+  const int mine = t1 - t0 - wave * KT;          // tiles from the wave's first on
+  const int steps = mine > 0 ? (mine + STRIDE - 1) / STRIDE : 0;
+  if (steps > 0) {
+    look_up(0);
+    fetch(0);
+    for (int k = 0; k < steps; ++k) {
+      KvRegs<FMT, D> now[KT];
+#pragma unroll
+      for (int j = 0; j < KT; ++j) now[j] = next[j];
+      const uint32_t have = there;
+      if (k + 1 < steps) {
+        if ((k + 1) % (64 / KT) == 0) look_up(k + 1);
+        fetch(k + 1);
+      }
+      const int base = (t0 + k * STRIDE + wave * KT) * 16;
+      if (have == (1u << KT) - 1 && base >= all_begin && base + 16 * KT <= all_end)
+        f.template step<false>(now, base, have, sp.n, a.scale2, g);
+      else
+        f.template step<true>(now, base, have, sp.n, a.scale2, g);
+    }
+  }
+
+  // Join the waves: factors from the maxima, sums one row tile at a time.
+  float* ml = lds + WAVES * 16 * (D + 4);        // [wave][row][2]
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float l = add_groups(f.l[t]);
+    if (g == 0) {
+      ml[(wave * NT * 16 + t * 16 + m) * 2] = f.m[t];
+      ml[(wave * NT * 16 + t * 16 + m) * 2 + 1] = l;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    __syncthreads();
+    float* mine_o = lds + (wave * 16 + m) * (D + 4);
+#pragma unroll
+    for (int sg = 0; sg < L::NSEG; ++sg)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int pr = 0; pr < L::lane(sg) / 2; ++pr) {
+          const int d = L::dim0(sg) / 16 + 2 * pr;
+          float* to = mine_o + L::dim0(sg) + (4 * g + i) * L::lane(sg) + 2 * pr;
+          to[0] = f.o[t][d][i];
+          to[1] = f.o[t][d + 1][i];
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 16 * D / 4; e += 64 * WAVES) {
+      const int rr = e / (D / 4), c = e % (D / 4) * 4, r = row0 + 16 * t + rr;
+      if (r >= rows) continue;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, ml[(w * NT * 16 + t * 16 + rr) * 2]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      float sum = 0;
+      f32x4_t o = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const float x = exp2_fast(ml[(w * NT * 16 + t * 16 + rr) * 2] - ref);
+        sum += x * ml[(w * NT * 16 + t * 16 + rr) * 2 + 1];
+        o += x * *reinterpret_cast<const f32x4_t*>(lds + (w * 16 + rr) * (D + 4) + c);
+      }
+      kv_store<DT>(a, sp, b, h, chunk, r, rows_all, D, c, o, top, sum);
+    }
+  }
+}
+
+template <int FMT, int D, int DT, int NT, int WAVES>
+hipError_t few_launch(const KvAttn& a, hipStream_t stream) {
+  const int64_t grid = (int64_t)a.batch * a.cache.heads * a.row_groups * a.chunks;
+  kv_few<FMT, D, DT, NT, WAVES><<<dim3((uint32_t)grid), dim3(64 * WAVES), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int FMT, int D, int DT>
+hipError_t few_by_rows(const KvAttn& a, const KvPlan& p, hipStream_t stream) {
+  if (p.rows == 16) return few_launch<FMT, D, DT, 1, kKvFewWaves>(a, stream);
+  if (p.rows == 32) return few_launch<FMT, D, DT, 2, kKvFewWaves>(a, stream);
+  if constexpr (kv_few_rows_most(DT, D) == 64)
+    if (p.rows == 64) return few_launch<FMT, D, DT, 4, kKvFewWaves>(a, stream);
+  return hipErrorInvalidValue;
+}
+
+template <int FMT, int DT>
+hipError_t few_by_dim(const KvAttn& a, int dim, const KvPlan& p, hipStream_t stream) {
+  switch (dim) {
+    case 64: return few_by_rows<FMT, 64, DT>(a, p, stream);
+    case 96: return few_by_rows<FMT, 96, DT>(a, p, stream);
+    case 128: return few_by_rows<FMT, 128, DT>(a, p, stream);
+    case 192: return few_by_rows<FMT, 192, DT>(a, p, stream);
+    case 256: return few_by_rows<FMT, 256, DT>(a, p, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace nc

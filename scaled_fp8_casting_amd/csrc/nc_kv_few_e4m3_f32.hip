@@ -1,0 +1,5 @@
+#include "nc_kv_few.h"
+
+namespace nc {
+hipError_t kv_few_e4m3_f32(const KvAttn& a, int dim, const KvPlan& p, hipStream_t s) { return few_by_dim<NC_E4M3, NC_F32>(a, dim, p, s); }
+}  // namespace nc

@@ -1,0 +1,206 @@
+"""nc_kv_attention against softmax attention in binary64 over what the cache holds."""
+
+import numpy as np
+import pytest
+import torch
+
+import scaled_fp8_casting_amd as nc
+from tests._kv import check, run_case
+
+pytestmark = pytest.mark.gpu
+
+DIMS = [64, 96, 128, 192, 256]
+
+
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_single_tokens(fmt, dtype, dim):
+    """The next token of sequences of length 1, around a tile, inside and past a page."""
+    check(*run_case(dim, fmt, dtype, dim, 2, 4, [1, 15, 16, 17, 48, 133, 259], [1] * 7, 48))
+
+
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_few_tokens(fmt, dtype, dim):
+    """Unequal numbers of queries, up to more rows than one row group; none for one sequence."""
+    check(*run_case(dim + 1, fmt, dtype, dim, 2, 3, [40, 77, 9, 200, 64], [5, 9, 0, 13, 2], 32))
+
+
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_prompt(fmt, dtype, dim):
+    """Prompts: all of a sequence's tokens, the end of a longer one, and fewer tokens than queries."""
+    check(*run_case(dim + 2, fmt, dtype, dim, 1, 2, [190, 300, 70], [190, 131, 150], 16))
+
+
+@pytest.mark.parametrize("fmt,dtype,dim", [("e2m1", "bf16", 128), ("e4m3", "bf16", 64), ("e4m3", "fp32", 96)])
+@pytest.mark.parametrize("lens,q_lens", [([33, 250], [170, 60]), ([1, 7], [1, 1]), ([80], [3])])
+def test_cross(fmt, dtype, dim, lens, q_lens):
+    check(*run_case(4, fmt, dtype, dim, 3, 1, lens, q_lens, 16, causal=False))
+
+
+@pytest.mark.parametrize("window", [1, 15, 16, 17, 64, 1000])
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [5, 3, 1], [90, 120, 7]])
+@pytest.mark.parametrize("causal", [True, False])
+def test_window(window, q_lens, causal):
+    check(*run_case(window, "e2m1", "bf16", 64, 2, 2, [300, 120, 40], q_lens, 16, causal=causal, window=window))
+
+
+@pytest.mark.parametrize("q_lens", [[9, 12], [70, 100]])
+@pytest.mark.parametrize("lens", [[3, 0], [0, 0], [1, 5]])
+def test_rows_that_see_nothing(lens, q_lens):
+    """More queries than cached tokens, and no tokens at all: out 0, lse -inf."""
+    check(*run_case(6, "e4m3", "bf16", 64, 1, 4, lens, q_lens, 16, max_kv=16))
+
+
+@pytest.mark.parametrize("group", [1, 5, 8, 16, 32])
+@pytest.mark.parametrize("n_q", [1, 4, 40])
+def test_groups(group, n_q):
+    check(*run_case(group, "e2m1", "bf16", 128, 1, group, [150, 61], [n_q, n_q], 64))
+
+
+@pytest.mark.parametrize("page", [16, 48, 64, 256])
+@pytest.mark.parametrize("n_q", [1, 100])
+def test_pages(page, n_q):
+    check(*run_case(page, "e2m1", "bf16", 128, 2, 2, [700, 333], [n_q, n_q], page))
+
+
+@pytest.mark.parametrize("fmt,dtype", [("e2m1", "bf16"), ("e4m3", "fp32")])
+@pytest.mark.parametrize("n_q", [1, 6, 80])
+def test_long_cache(fmt, dtype, n_q):
+    """Enough tokens that a sequence's keys are cut over workgroups and joined."""
+    check(*run_case(8, fmt, dtype, 64, 1, 2, [9000, 2600], [n_q, n_q], 64))
+
+
+@pytest.mark.parametrize("n_q", [1, 100])
+def test_long_cache_with_window(n_q):
+    check(*run_case(9, "e2m1", "bf16", 64, 1, 2, [9000, 600, 5000], [n_q, n_q, n_q], 32, window=2500))
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.0, -0.5, 3.0])
+@pytest.mark.parametrize("n_q", [1, 90])
+def test_scale(scale, n_q):
+    """Weights of a softmax near a maximum, equal weights, and a negative scale."""
+    check(*run_case(10, "e4m3", "fp32", 64, 2, 1, [130, 50], [n_q, n_q], 16, scale=scale))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n_q", [1, 100])
+def test_strided_queries_and_outputs(dtype, n_q):
+    check(*run_case(12, "e2m1", dtype, 96, 2, 3, [77, 210], [n_q, n_q], 16, sliced=True))
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("n_q", [1, 6, 100])
+def test_nan_reaches_only_rows_that_see_it(fmt, n_q):
+    """A NaN key makes rows that see it NaN; a NaN value its elements (E2M1: its block) in
+    them.  Rows that do not see it keep their results."""
+    def mutate(k, v, q):
+        k[110, 0, 5] = float("nan")
+        v[114, 1, 37] = float("nan")
+    check(*run_case(13, fmt, "bf16", 64, 2, 2, [120, 40], [n_q, n_q], 16, mutate=mutate))
+
+
+def test_large_scores():
+    """Scores far apart: most weights underflow, none overflows."""
+    def mutate(k, v, q):
+        q *= 40
+    check(*run_case(14, "e4m3", "fp32", 64, 1, 1, [300], [3], 16, mutate=mutate))
+    check(*run_case(14, "e4m3", "fp32", 64, 1, 1, [300], [100], 16, mutate=mutate))
+
+
+@pytest.mark.parametrize("n_q", [1, 80])
+def test_device_arrays_are_not_trusted(n_q):
+    """Pages outside the cache are not seen; lengths and offsets that do not fit are cut; the
+    rows of a sequence without queries are left alone."""
+    dim, page, heads = 64, 16, 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache = nc.new_kv_cache(4, page, heads, dim, "e4m3")
+    k = torch.randn(64, heads, dim, generator=g, device="cuda").bfloat16()
+    v = torch.randn(64, heads, dim, generator=g, device="cuda").bfloat16()
+    nc.nc_kv_write(cache, k, v, torch.arange(64, device="cuda"))
+    q = torch.randn(2 * n_q, 2, dim, generator=g, device="cuda").bfloat16()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def call(starts, lens, table, causal=False, max_kv=64):
+        out, lse = torch.full_like(q, 5.0), torch.full((2 * n_q, 2), 5.0, device="cuda")
+        nc.nc_kv_attention(cache, q, out, starts, lens, table, n_q, max_kv, causal=causal, lse=lse)
+        torch.cuda.synchronize()
+        return out, lse
+
+    whole = i32([0, 1, 2, 3], [3, 2, 1, 0])
+    good = call(i32(0, n_q, 2 * n_q), i32(32, 32), whole)
+    # pages 1 and 2 of the first sequence lie outside the cache: the same as its first 16 tokens alone
+    bad = call(i32(0, n_q, 2 * n_q), i32(48, 32), i32([0, -1, 4, 3], [3, 2, 1, 0]))
+    short = call(i32(0, n_q, 2 * n_q), i32(16, 32), whole)
+    assert torch.equal(bad[0], short[0]) and torch.equal(bad[1], short[1])
+    # lengths above max_kv and above the table, and negative ones
+    cut = call(i32(0, n_q, 2 * n_q), i32(32, 999), i32([0, 1], [3, 2]))
+    assert torch.equal(cut[0], good[0]) and torch.equal(cut[1], good[1])
+    cut = call(i32(0, n_q, 2 * n_q), i32(99, 2 ** 31 - 1), whole, max_kv=32)
+    assert torch.equal(cut[0], good[0]) and torch.equal(cut[1], good[1])
+    none = call(i32(0, n_q, 2 * n_q), i32(32, -7), whole)
+    assert torch.equal(none[0][:n_q], good[0][:n_q])
+    assert not none[0][n_q:].any() and torch.isneginf(none[1][n_q:]).all()
+    # offsets that leave q: no queries
+    for starts in (i32(0, n_q, 2 * n_q + 1), i32(0, n_q, 0), i32(-1, n_q, n_q)):
+        o, l = call(starts, i32(32, 32), whole)
+        assert (o[n_q:] == 5).all() and (l[n_q:] == 5).all()
+
+
+@pytest.mark.parametrize("n_q,kv", [(1, 3000), (1, 100), (70, 1500)])
+def test_stream_graph_and_same_bits(n_q, kv):
+    """On a stream of its own, captured and replayed with new inputs; the same call gives the same bits."""
+    dim, page, heads = 128, 64, 2
+    g = torch.Generator(device="cuda").manual_seed(2)
+    pages = -(-kv // page)
+    cache = nc.new_kv_cache(pages, page, heads, dim, "e2m1")
+    k, v = (torch.randn(kv, heads, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    slots = torch.arange(kv, device="cuda")
+    q = torch.randn(n_q, 4 * heads, dim, generator=g, device="cuda").bfloat16()
+    starts = torch.tensor([0, n_q], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([kv], dtype=torch.int32, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    out, lse = torch.empty_like(q), torch.empty(n_q, 4 * heads, device="cuda")
+    ws = nc.new_kv_workspace(cache, q, 1, n_q, kv)
+
+    def step(o, l, stream=None, w=ws):
+        nc.nc_kv_write(cache, k, v, slots, stream=stream)
+        nc.nc_kv_attention(cache, q, o, starts, lens, table, n_q, kv, lse=l, ws=w, stream=stream)
+
+    step(out, lse)
+    torch.cuda.synchronize()
+    first = out.clone(), lse.clone()
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    step(o2, l2, s, None)                         # a workspace of the call's own
+    s.synchronize()
+    assert torch.equal(o2, first[0]) and torch.equal(l2, first[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out, lse)
+    for i in range(4):
+        q.copy_(torch.randn(q.shape, generator=g, device="cuda"))
+        k.copy_(torch.randn(k.shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), lse.clone()
+        step(o2, l2)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], o2) and torch.equal(got[1], l2), i
+
+
+def test_empty_calls():
+    cache = nc.new_kv_cache(1, 16, 1, 64, "e2m1")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.empty((0, 1, 64), dtype=torch.bfloat16, device="cuda")
+    nc.nc_kv_attention(cache, q, q.clone(), i32(0), i32(), torch.empty((0, 0), dtype=torch.int32, device="cuda"), 0, 0)
+    q = torch.ones((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, 3.0), torch.full((1, 1), 3.0, device="cuda")
+    # a table without pages: nothing to see
+    nc.nc_kv_attention(cache, q, out, i32(0, 1), i32(9), torch.empty((1, 0), dtype=torch.int32, device="cuda"), 1, 9, lse=lse)
+    assert not out.any() and torch.isneginf(lse).all()
