@@ -111,7 +111,6 @@ struct KvAttn {
 // size and the launch.
 struct KvPlan {
   int32_t rows;         // rows of a workgroup
-  int32_t waves;        // waves of a workgroup
   int32_t row_groups;   // workgroups along the rows of one (sequence, head)
   int32_t chunk;        // tiles of 16 keys of a workgroup
   int32_t chunks;       // workgroups along the keys, at most `most`
@@ -119,6 +118,7 @@ struct KvPlan {
 };
 
 constexpr int kKvFewWaves = 4;
+constexpr int kKvManyRows = 128;   // rows of a workgroup of the many-row kernel
 // Most rows of a workgroup of the few-row kernel: 64 where queries, sums and a
 // step's codes fit the registers of two waves a SIMD or one, else 32.
 constexpr int kv_few_rows_most(int dtype, int dim) { return dtype == NC_BF16 && dim <= 128 ? 64 : 32; }
@@ -138,6 +138,10 @@ hipError_t kv_few_e2m1_bf16(const KvAttn& a, int dim, const KvPlan& p, hipStream
 hipError_t kv_few_e2m1_f32(const KvAttn& a, int dim, const KvPlan& p, hipStream_t stream);
 hipError_t kv_few_e4m3_bf16(const KvAttn& a, int dim, const KvPlan& p, hipStream_t stream);
 hipError_t kv_few_e4m3_f32(const KvAttn& a, int dim, const KvPlan& p, hipStream_t stream);
+hipError_t kv_many_e2m1_bf16(const KvAttn& a, int dim, hipStream_t stream);
+hipError_t kv_many_e2m1_f32(const KvAttn& a, int dim, hipStream_t stream);
+hipError_t kv_many_e4m3_bf16(const KvAttn& a, int dim, hipStream_t stream);
+hipError_t kv_many_e4m3_f32(const KvAttn& a, int dim, hipStream_t stream);
 hipError_t launch_kv_join(const KvAttn& a, int dim, int dtype, hipStream_t stream);
 
 }  // namespace nc

@@ -53,13 +53,13 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
 // The split of a call.  span: tiles of 16 keys that a row group may reach.
 KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_t rows_all, int64_t span) {
   KvPlan p;
-  p.waves = kKvFewWaves;
-  const int most = kv_few_rows_most(dtype, dim);
-  p.rows = rows_all <= 16 ? 16 : (rows_all <= 32 || most == 32 ? 32 : 64);
+  const int few = kv_few_rows_most(dtype, dim);
+  const bool many = rows_all > few;
+  p.rows = many ? kKvManyRows : (rows_all <= 16 ? 16 : (rows_all <= 32 ? 32 : 64));
   p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
   const int64_t base = std::max<int64_t>(1, batch * heads * p.row_groups);
-  // at least 32 tiles (512 keys) each, at most about 1024 workgroups
-  const int64_t want = std::min<int64_t>((1024 + base - 1) / base, span / 32);
+  // few rows: at least 32 tiles (512 keys) each, at most about 1024 workgroups; many: 16 tiles, 512 workgroups
+  const int64_t want = many ? std::min<int64_t>(512 / base, span / 16) : std::min<int64_t>((1024 + base - 1) / base, span / 32);
   const int64_t chunks = std::max<int64_t>(1, want);
   p.most = (int32_t)chunks;
   p.chunk = (int32_t)std::max<int64_t>(1, (span + chunks - 1) / chunks);
@@ -165,8 +165,14 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   }
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e;
-  if (c->fmt == NC_E2M1) e = dtype == NC_BF16 ? kv_few_e2m1_bf16(k, c->dim, p, st) : kv_few_e2m1_f32(k, c->dim, p, st);
-  else e = dtype == NC_BF16 ? kv_few_e4m3_bf16(k, c->dim, p, st) : kv_few_e4m3_f32(k, c->dim, p, st);
+  const bool b16 = dtype == NC_BF16;
+  if (p.rows == kKvManyRows) {
+    if (c->fmt == NC_E2M1) e = b16 ? kv_many_e2m1_bf16(k, c->dim, st) : kv_many_e2m1_f32(k, c->dim, st);
+    else e = b16 ? kv_many_e4m3_bf16(k, c->dim, st) : kv_many_e4m3_f32(k, c->dim, st);
+  } else {
+    if (c->fmt == NC_E2M1) e = b16 ? kv_few_e2m1_bf16(k, c->dim, p, st) : kv_few_e2m1_f32(k, c->dim, p, st);
+    else e = b16 ? kv_few_e4m3_bf16(k, c->dim, p, st) : kv_few_e4m3_f32(k, c->dim, p, st);
+  }
   if (e == hipSuccess && p.chunks > 1) e = launch_kv_join(k, c->dim, dtype, st);
   return hip_status(e);
 }
