@@ -44,14 +44,38 @@ __device__ __forceinline__ f32x4_t mfma16(const u32x4& a, const u32x4& b, const 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// Maximum and sum over the lanes l, l ^ 16, l ^ 32, l ^ 48.
+// Maximum and sum over the lanes l, l ^ 32 and over l, l ^ 16, l ^ 32, l ^ 48:
+// a swap of half waves (or of rows of 16 lanes) of two copies puts both
+// partners' values into every lane.
+__device__ __forceinline__ void swap_halves(float x, float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap_rows(float x, float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max_halves(float x) {
+  float a, b;
+  swap_halves(x, a, b);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ float add_halves(float x) {
+  float a, b;
+  swap_halves(x, a, b);
+  return a + b;
+}
 __device__ __forceinline__ float max_groups(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+  float a, b;
+  swap_rows(x, a, b);
+  return max_halves(fmaxf(a, b));
 }
 __device__ __forceinline__ float add_groups(float x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
+  float a, b;
+  swap_rows(x, a, b);
+  return add_halves(a + b);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -140,7 +140,7 @@ template <int FMT, int D, int DT> struct Many {
         top = fmaxf(top, s[j][i]);
       }
     }
-    top = fmaxf(top, __shfl_xor(top, 32)) * scale2;
+    top = max_halves(top) * scale2;
     if (MASKED && !(top > -INFINITY)) top = -INFINITY;       // 0 scale times no key
     if (__ballot(top > m + kManyGrowth)) {
       const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
@@ -243,13 +243,12 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   const int t0 = any_begin / 16 + chunk * a.chunk;
   const int t1 = min((any_end + 15) >> 4, t0 + a.chunk);
 
-  // this wave's rows, and the keys that some and all of them see
+  // this wave's rows, and the keys that some of them see
   const int wrow = row0 + 32 * wave, r = wrow + n;
   const bool live = r < rows;
   const int i = live ? r / a.group : 0, j = live ? r - i * a.group : 0;
   const int w_lo = min(wrow, rows - 1) / a.group, w_hi = (min(rows, wrow + 32) - 1) / a.group;
-  const int w_any_end = wrow < rows ? kv_end(a, sp, w_hi) : 0, w_all_end = kv_end(a, sp, w_lo);
-  const int w_any_begin = kv_begin(a, w_all_end), w_all_begin = kv_begin(a, kv_end(a, sp, w_hi));
+  const int w_any_end = wrow < rows ? kv_end(a, sp, w_hi) : 0, w_any_begin = kv_begin(a, kv_end(a, sp, w_lo));
 
   Many<FMT, D, DT> f;
   f.end = kv_end(a, sp, i);
@@ -271,58 +270,80 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
     for (int c = 0; c < Many<FMT, D, DT>::QP; ++c) f.q[st][c] ^= flip;
   }
 
+  // Steps [0, ka) and [kb, steps) have masks for some row; those between have none: whole, seen by
+  // every row, no page missing.
   const int tiles = max(t1 - t0, 0), steps = (tiles + 3) / 4;
+  int ka = steps, kb = steps;
+  {
+    bool miss = false;
+    for (int t = t0 + (int)threadIdx.x; t < t1; t += 64 * kManyWaves) miss = miss || kv_tile_at(a, b, h, t) < 0;
+    const int first = max(kv_begin(a, any_end) - 16 * t0, 0), last = min(kv_end(a, sp, i_lo) - 16 * t0, 16 * tiles);
+    if (!__syncthreads_or(miss) && last > first) {
+      ka = (first + kManyKeys - 1) / kManyKeys;
+      kb = max(ka, last / kManyKeys);
+    }
+  }
   // Lane x looks up this wave's tile of step first + x, 64 steps at a time.
   int ids = -1;
+  bool there = false;
   KvRegs<FMT, D> next;
-  auto fetch = [&](int k) -> bool {
-    if ((k & 63) == 0) {
-      const int t = t0 + 4 * (k + lane) + wave;
-      ids = t < t1 ? kv_tile_at(a, b, h, t) : -1;
-    }
-    const int tile = __builtin_amdgcn_readlane(ids, k & 63);
-    load_tile<FMT, D>(next, a.cache.data + (int64_t)max(tile, 0) * L::TILE, lane & 15, lane >> 4);
-    return tile >= 0;
-  };
-  // whether a step needs no mask in any wave: whole, seen by every row, no page missing
-  // (a page missing is known to its wave only, so it is noted in LDS)
   __shared__ uint32_t have[2][kManyWaves];
-  auto put = [&](int k, bool there) {
-    const int base = (t0 + 4 * k) * 16;
-    const bool whole = base + kManyKeys <= kv_end(a, sp, i_lo) && base >= kv_begin(a, any_end) && 4 * k + 4 <= tiles;
-    if (lane == 0) have[k & 1][wave] = there;
-    if (whole && there) {
-      if (lane == 0) lds[k & 1].bad[wave] = 1;       // not looked at
+  auto look_up = [&](int k) {
+    const int t = t0 + 4 * (k + lane) + wave;
+    ids = t < t1 ? kv_tile_at(a, b, h, t) : -1;
+  };
+  auto fetch = [&](int k) {                      // past the last step: the cache's first tile, unused
+    const int tile = __builtin_amdgcn_readlane(ids, k & 63);
+    there = tile >= 0;
+    load_tile<FMT, D>(next, a.cache.data + (int64_t)max(tile, 0) * L::TILE, lane & 15, lane >> 4);
+  };
+  auto put = [&](int k) {
+    if (k >= ka && k < kb) {
       stage<FMT, D, false>(lds[k & 1], next, wave, lane, true, 16);
     } else {
-      stage<FMT, D, true>(lds[k & 1], next, wave, lane, there, sp.n - base - 16 * wave);
+      if (lane == 0) have[k & 1][wave] = there;
+      stage<FMT, D, true>(lds[k & 1], next, wave, lane, there, sp.n - (t0 + 4 * k + wave) * 16);
     }
   };
-  if (steps > 0) {
-    bool there = fetch(0);
-    put(0, there);
-    if (steps > 1) there = fetch(1);
-    for (int k = 0; k < steps; ++k) {
-      __syncthreads();
-      if (k + 1 < steps) {
-        put(k + 1, there);
-        if (k + 2 < steps) there = fetch(k + 2);
-      }
-      const int base = (t0 + 4 * k) * 16;
-      if (base >= w_any_end || base + kManyKeys <= w_any_begin) continue;
-      uint32_t all = 0;
+  auto masked = [&](int k) {
+    if (((k + 2) & 63) == 0) look_up(k + 2);
+    __syncthreads();
+    if (k + 1 < steps) put(k + 1);
+    fetch(k + 2);
+    const int base = (t0 + 4 * k) * 16;
+    if (base >= w_any_end || base + kManyKeys <= w_any_begin) return;
+    uint32_t all = 0;
 #pragma unroll
-      for (int w = 0; w < kManyWaves; ++w) all |= have[k & 1][w] ? 1u << w : 0u;
-      all = __builtin_amdgcn_readfirstlane(all);
-      if (all == (1u << kManyWaves) - 1 && base + kManyKeys <= w_all_end && base >= w_all_begin)
-        f.template step<false>(lds[k & 1], base, all, scale2, lane);
-      else
-        f.template step<true>(lds[k & 1], base, all, scale2, lane);
+    for (int w = 0; w < kManyWaves; ++w) all |= have[k & 1][w] ? 1u << w : 0u;
+    f.template step<true>(lds[k & 1], base, __builtin_amdgcn_readfirstlane(all), scale2, lane);
+  };
+  if (steps > 0) {
+    look_up(0);
+    fetch(0);
+    put(0);
+    fetch(1);
+    int k = 0;
+    for (; k < ka; ++k) masked(k);
+    for (; k + 1 < kb; ++k) {
+      if (((k + 2) & 63) == 0) look_up(k + 2);
+      __syncthreads();
+      stage<FMT, D, false>(lds[(k + 1) & 1], next, wave, lane, true, 16);
+      fetch(k + 2);
+      f.template step<false>(lds[k & 1], 0, 0, scale2, lane);
     }
+    if (k < kb) {                                // the last of them, before one that may have masks
+      if (((k + 2) & 63) == 0) look_up(k + 2);
+      __syncthreads();
+      if (k + 1 < steps) put(k + 1);
+      fetch(k + 2);
+      f.template step<false>(lds[k & 1], 0, 0, scale2, lane);
+      ++k;
+    }
+    for (; k < steps; ++k) masked(k);
   }
 
   // results: a lane holds, of its row, the elements with lane index m = 8 x + 4 h2 + 0..3 of every tile
-  const float l = f.l + __shfl_xor(f.l, 32);
+  const float l = add_halves(f.l);
   if (!live) return;
 #pragma unroll
   for (int sg = 0; sg < L::NSEG; ++sg) {
