@@ -457,19 +457,18 @@ _KV_DTYPE = {torch.float32: (NC_F32, 4), torch.bfloat16: (NC_BF16, 8)}     # cod
 
 
 def _rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, unit: int, dev: torch.device):
-    """Token and head stride of [tokens, heads, dim] rows: any that are multiples of 16 bytes, elements adjacent."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, the cache is on {dev}")
+    """Pointer, token and head stride of [tokens, heads, dim] rows: strides that are multiples of 16 bytes,
+    elements adjacent.  The pointer is checked to be the device's by the caller."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} of {t.dtype} on {t.device}, expected {tuple(shape)} of "
+                         f"{dtype} on {dev}")
     ts, hs, one = t.stride()
+    at = t.data_ptr()
     if shape[0] <= 1:
         ts = 0
-    if one != 1 or (ts | hs) & (unit - 1) or t.data_ptr() & 15:
+    if one != 1 or (ts | hs) & (unit - 1) or at & 15:
         raise ValueError(f"{name}: strides {t.stride()}: rows of adjacent elements that start on 16 bytes expected")
-    return ts, hs
+    return at, ts, hs
 
 
 def _spread(t: torch.Tensor, name: str):
@@ -485,24 +484,25 @@ def _spread(t: torch.Tensor, name: str):
 
 def _kv_stream(stream, dev: torch.device) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev.index)     # torch.cuda.current_stream(dev), without its object
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _kv_tokens(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
     """Checks of a write or read; the call's arguments from the cache to the slots."""
-    if k.dtype not in _KV_DTYPE:
-        raise TypeError(f"dtype {k.dtype} (float32 or bfloat16 expected)")
-    code, unit = _KV_DTYPE[k.dtype]
-    dev = cache.device
-    if slots.dim() != 1 or slots.device != dev:
-        raise ValueError(f"slots: shape {tuple(slots.shape)} on {slots.device}, expected one entry a token on {dev}")
+    dt, dev = k.dtype, cache.device
+    if dt not in _KV_DTYPE:
+        raise TypeError(f"dtype {dt} (float32 or bfloat16 expected)")
+    code, unit = _KV_DTYPE[dt]
+    if slots.dtype is not torch.int64 or slots.dim() != 1 or slots.device != dev or not slots.is_contiguous():
+        raise ValueError(f"slots: shape {tuple(slots.shape)} of {slots.dtype} on {slots.device}, expected contiguous "
+                         f"torch.int64, one entry a token, on {dev}")
     tokens = slots.shape[0]
-    if slots.dtype is not torch.int64 or not slots.is_contiguous():
-        raise ValueError(f"slots: dtype {slots.dtype}, expected contiguous torch.int64")
-    shape = torch.Size((tokens, cache.heads, cache.dim))
-    ks, vs = _rows(k, "k", shape, k.dtype, unit, dev), _rows(v, "v", shape, k.dtype, unit, dev)
-    return (cache.descriptor, NcKvRows(_ptr(k), *ks), NcKvRows(_ptr(v), *vs), tokens, code, _ptr(slots))
+    shape = (tokens, cache.heads, cache.dim)
+    ks, vs = _rows(k, "k", shape, dt, unit, dev), _rows(v, "v", shape, dt, unit, dev)
+    if dev.type != "cuda":
+        raise ValueError("device tensor expected (no CPU path)")
+    return cache.descriptor, NcKvRows(*ks), NcKvRows(*vs), tokens, code, slots.data_ptr()
 
 
 def nc_kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule="ceil", stream=None):
@@ -546,42 +546,47 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
     (cross attention).  window: tokens that a query sees at most, 0 for all.
     scale: 1 / sqrt(dim) where None.  lse (fp32 [rows, q_heads]) receives
     log sum exp of the scores; a query that sees nothing gets out 0, lse -inf."""
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"q: dtype {q.dtype} (float32 or bfloat16 expected)")
-    if q.dim() != 3:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected (rows, q_heads, {cache.dim})")
-    rows, q_heads, _ = q.shape
-    dev = cache.device
+    dt, dev, shape = q.dtype, cache.device, q.shape
+    if dt not in _KV_DTYPE:
+        raise TypeError(f"q: dtype {dt} (float32 or bfloat16 expected)")
+    if len(shape) != 3 or shape[2] != cache.dim:
+        raise ValueError(f"q: shape {tuple(shape)}, expected (rows, q_heads, {cache.dim})")
+    rows, q_heads, _ = shape
     if q_heads == 0 or q_heads % cache.heads:
         raise ValueError(f"q: {q_heads} heads, a multiple of the cache's {cache.heads} expected")
-    code, unit = _KV_DTYPE[q.dtype]
-    shape = torch.Size((rows, q_heads, cache.dim))
-    qs, os = _rows(q, "q", shape, q.dtype, unit, dev), _rows(out, "out", shape, q.dtype, unit, dev)
+    code, unit = _KV_DTYPE[dt]
+    qs, os = _rows(q, "q", shape, dt, unit, dev), _rows(out, "out", shape, dt, unit, dev)
     _spread(out, "out")
     batch = kv_len.numel()
-    for t, name, n in ((q_start, "q_start", batch + 1), (kv_len, "kv_len", batch)):
-        if t.dtype is not torch.int32 or t.shape != (n,) or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: shape {tuple(t.shape)} of {t.dtype} on {t.device}, expected contiguous torch.int32 "
-                             f"({n},) on {dev}")
-    if table.dtype is not torch.int32 or table.dim() != 2 or table.shape[0] != batch or not table.is_contiguous() \
-            or table.device != dev:
+    i32 = torch.int32
+    if kv_len.dtype is not i32 or kv_len.dim() != 1 or kv_len.device != dev or not kv_len.is_contiguous():
+        raise ValueError(f"kv_len: shape {tuple(kv_len.shape)} of {kv_len.dtype} on {kv_len.device}, expected contiguous "
+                         f"torch.int32 (batch,) on {dev}")
+    if q_start.dtype is not i32 or q_start.shape != (batch + 1,) or q_start.device != dev or not q_start.is_contiguous():
+        raise ValueError(f"q_start: shape {tuple(q_start.shape)} of {q_start.dtype} on {q_start.device}, expected "
+                         f"contiguous torch.int32 ({batch + 1},) on {dev}")
+    if table.dtype is not i32 or table.dim() != 2 or table.shape[0] != batch or table.device != dev \
+            or not table.is_contiguous():
         raise ValueError(f"table: shape {tuple(table.shape)} of {table.dtype} on {table.device}, expected contiguous "
                          f"torch.int32 ({batch}, pages) on {dev}")
     if max_q < 0 or max_kv < 0 or window < 0:
         raise ValueError(f"max_q {max_q}, max_kv {max_kv}, window {window}: none may be negative")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.dim)
-    if not math.isfinite(scale):
+    elif not math.isfinite(scale):
         raise ValueError(f"scale {scale}: a finite number expected")
-    lts = 0
+    lat, lts = None, 0
     if lse is not None:
-        if lse.dtype is not torch.float32 or lse.shape != shape[:2] or lse.device != dev \
+        if lse.dtype is not torch.float32 or lse.shape != (rows, q_heads) or lse.device != dev \
                 or (q_heads > 1 and lse.stride(1) != 1):
             raise ValueError(f"lse: shape {tuple(lse.shape)} of {lse.dtype} on {lse.device}, expected torch.float32 "
                              f"({rows}, {q_heads}) on {dev}, heads adjacent")
         _spread(lse, "lse")
-        lts = lse.stride(0) if rows > 1 else 0
-    _need(ws, "ws", torch.uint8, 0)
+        lat, lts = lse.data_ptr(), (lse.stride(0) if rows > 1 else 0)
+    if ws is not None and (ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws: dtype {ws.dtype} on {ws.device}, expected contiguous torch.uint8 on {dev}")
+    if dev.type != "cuda":
+        raise ValueError("device tensor expected (no CPU path)")
     if rows == 0 or batch == 0 or max_q == 0:
         return
     c = cache.descriptor
@@ -594,7 +599,7 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
                 stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev))
             with torch.cuda.stream(on):
                 ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    a = NcKvAttn(_ptr(q), *qs, _ptr(out), *os, _ptr(lse), lts, _ptr(q_start), _ptr(kv_len), _ptr(table), table.shape[1],
-                 batch, rows, q_heads, max_q, max_kv, 1 if causal else 0, window, scale)
-    _check(lib.nc_kv_attention(c, a, code, _ptr(ws), 0 if ws is None else ws.numel(), _kv_stream(stream, dev)),
-           "nc_kv_attention")
+    a = NcKvAttn(*qs, *os, lat, lts, q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), table.shape[1], batch, rows,
+                 q_heads, max_q, max_kv, 1 if causal else 0, window, scale)
+    wat, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    _check(lib.nc_kv_attention(c, a, code, wat, wn, _kv_stream(stream, dev)), "nc_kv_attention")

@@ -119,9 +119,8 @@ struct KvPlan {
 
 constexpr int kKvFewWaves = 4;
 constexpr int kKvManyRows = 128;   // rows of a workgroup of the many-row kernel
-// Most rows of a workgroup of the few-row kernel: 64 where queries, sums and a
-// step's codes fit the registers of two waves a SIMD or one, else 32.
-constexpr int kv_few_rows_most(int dtype, int dim) { return dtype == NC_BF16 && dim <= 128 ? 64 : 32; }
+// Most rows of a workgroup of the few-row kernel: 32 where their queries and sums fit the registers.
+constexpr int kv_few_rows(int dtype, int dim) { return dtype == NC_BF16 || dim <= 128 ? 32 : 16; }
 
 // Rows (query i of the sequence, head j of the group) are numbered i * group + j.
 // Partial results of chunk c, sequence b, head h, row r: D unnormalised sums, at

@@ -53,9 +53,8 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
 // The split of a call.  span: tiles of 16 keys that a row group may reach.
 KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_t rows_all, int64_t span) {
   KvPlan p;
-  const int few = kv_few_rows_most(dtype, dim);
-  const bool many = rows_all > few;
-  p.rows = many ? kKvManyRows : (rows_all <= 16 ? 16 : (rows_all <= 32 ? 32 : 64));
+  const bool many = rows_all > 32;
+  p.rows = many ? kKvManyRows : (rows_all <= 16 ? 16 : kv_few_rows(dtype, dim));
   p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
   const int64_t base = std::max<int64_t>(1, batch * heads * p.row_groups);
   // few rows: at least 32 tiles (512 keys) each, at most about 1024 workgroups; many: 16 tiles, 512 workgroups

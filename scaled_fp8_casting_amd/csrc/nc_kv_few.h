@@ -158,15 +158,23 @@ __device__ __forceinline__ void load_dwords(uint32_t* r, const uint8_t* p) {
 }
 
 template <int FMT, int D, int S = 0>
-__device__ __forceinline__ void load_tile(KvRegs<FMT, D>& r, const uint8_t* t, int m, int g) {
+__device__ __forceinline__ void load_keys(KvRegs<FMT, D>& r, const uint8_t* t, int m, int g) {
   using L = Kv<FMT, D>;
   if constexpr (S < L::NSEG) {
     constexpr int w = L::w(S), off = L::off(S), n = w / 16;
     load_dwords<n>(r.k + off / 16, t + L::KC + 16 * off + (g * 16 + m) * (w / 4));
-    load_dwords<n>(r.v + off / 16, t + L::VC + 16 * off + (g * 16 + m) * (w / 4));
     r.ks[S] = t[L::KS + ((L::dim0(S) + g * L::piece(S)) / 32) * 16 + m];
+    load_keys<FMT, D, S + 1>(r, t, m, g);
+  }
+}
+template <int FMT, int D, int S = 0>
+__device__ __forceinline__ void load_values(KvRegs<FMT, D>& r, const uint8_t* t, int m, int g) {
+  using L = Kv<FMT, D>;
+  if constexpr (S < L::NSEG) {
+    constexpr int w = L::w(S), off = L::off(S), n = w / 16;
+    load_dwords<n>(r.v + off / 16, t + L::VC + 16 * off + (g * 16 + m) * (w / 4));
     r.vs[S] = *reinterpret_cast<const uint32_t*>(t + L::VS + ((L::dim0(S) + m * L::lane(S)) / 32) * 16 + 4 * g);
-    load_tile<FMT, D, S + 1>(r, t, m, g);
+    load_values<FMT, D, S + 1>(r, t, m, g);
   }
 }
 
@@ -217,34 +225,33 @@ __device__ __forceinline__ uint32_t whole16(uint32_t x) {
   return (x & 0xFFFFu ? 0xFFFFu : 0u) | (x & 0xFFFF0000u ? 0xFFFF0000u : 0u);
 }
 
-// Tiles of 16 keys that a wave takes at a time: 4 while the raw codes of a
-// step stay within 40 registers, else 2.
-template <int FMT, int D> constexpr int few_tiles() { return Kv<FMT, D>::DW <= 4 ? 4 : 2; }
+// The running reference m of a row follows its maximum only when that has
+// grown by more than 2^8: weights then stay below 2^8 and the sums are
+// rescaled a few times per call instead of at every new maximum.
+constexpr float kGrowth = 8.0f;
+
+constexpr int kFewTiles = 2;                     // tiles of 16 keys that a wave takes at a time
 
 template <int FMT, int D, int DT, int NT> struct Few {
   using L = Kv<FMT, D>;
-  static constexpr int QP = QParts<DT>::N;       // parts of a query
-  static constexpr int PP = QP;                  // parts of a weight
-  static constexpr int KT = few_tiles<FMT, D>();
+  static constexpr int QP = QParts<DT>::N;       // parts of a query, and of a weight
+  static constexpr int KT = kFewTiles;
   static constexpr int MT = D / 16;              // output tiles of 16 elements
 
   u32x4 q[NT][D / 32][QP];
   f32x4_t o[NT][MT];
-  float m[NT], l[NT];                            // l: this lane's keys only
+  f32x4_t s[NT][KT];                             // scores
+  u32x4 p[NT][QP];                               // weights
+  float m[NT], l[NT];                            // reference; sum of this lane's keys
   int end[NT], begin[NT];                        // keys that the lane's row sees
 
-  // One step of KT tiles.  base: key of the first; MASKED: some row sees some
-  // key of the step not, or a tile is missing (bit of `there` off).
-  template <bool MASKED>
-  __device__ __forceinline__ void step(const KvRegs<FMT, D> (&r)[KT], int base, uint32_t there, int n_keys, float scale2,
-                                       int g) {
-    f32x4_t s[NT][KT];
+  __device__ __forceinline__ void scores(const KvRegs<FMT, D> (&r)[KT]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int j = 0; j < KT; ++j) s[t][j] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < KT; ++j) {
+    for (int j = 0; j < KT; ++j)
 #pragma unroll
       for (int sg = 0; sg < L::NSEG; ++sg) {
         const float sc = kv_scale(r[j].ks[sg]);
@@ -261,8 +268,11 @@ template <int FMT, int D, int DT, int NT> struct Few {
             for (int c2 = QP - 1; c2 >= 0; --c2) s[t][j] = mfma16(a, q[t][L::dim0(sg) / 32 + st][c2], s[t][j]);
         }
       }
-    }
-    u32x4 p[NT][KT / 2][PP];
+  }
+
+  // MASKED: some row sees some key of the step not, or a tile is missing (bit of `there` off).
+  template <bool MASKED>
+  __device__ __forceinline__ void weights(int base, uint32_t there, float scale2, int g) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float top = -INFINITY;
@@ -270,120 +280,123 @@ template <int FMT, int D, int DT, int NT> struct Few {
       for (int j = 0; j < KT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x = s[t][j][i] * scale2;
           if constexpr (MASKED) {
             const int key = base + 16 * j + 4 * g + i;
-            x = key < end[t] && key >= begin[t] && ((there >> j) & 1) ? x : -INFINITY;
+            s[t][j][i] = key < end[t] && key >= begin[t] && ((there >> j) & 1) ? s[t][j][i] : -INFINITY;
           }
-          s[t][j][i] = x;
-          top = fmaxf(top, x);
+          top = fmaxf(top, s[t][j][i]);
         }
-      top = max_groups(top);
-      const float mn = fmaxf(m[t], top);
-      const float ref = mn == -INFINITY ? 0.0f : mn;
-      if (__ballot(mn != m[t])) {
-        const float f = exp2_fast(m[t] - ref);
+      top = max_groups(top) * scale2;
+      if (MASKED && !(top > -INFINITY)) top = -INFINITY;       // 0 scale times no key
+      if (__ballot(top > m[t] + kGrowth)) {
+        const float mn = fmaxf(m[t], top), f = m[t] == -INFINITY ? 0.0f : exp2_fast(m[t] - mn);
         l[t] *= f;
 #pragma unroll
         for (int d = 0; d < MT; ++d) o[t][d] *= f;
         m[t] = mn;
       }
+      const float ref = m[t] == -INFINITY ? 0.0f : m[t];
       float sum = 0;
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          e[i] = exp2_fast(s[t][j][i] - ref);
+          e[i] = exp2_fast(__builtin_fmaf(s[t][j][i], scale2, -ref));
+          if constexpr (MASKED) {
+            const int key = base + 16 * j + 4 * g + i;
+            e[i] = key < end[t] && key >= begin[t] && ((there >> j) & 1) ? e[i] : 0.0f;
+          }
           sum += e[i];
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if constexpr (PP == 1) {
-            p[t][j / 2][0][2 * (j & 1) + i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+          if constexpr (QP == 1) {
+            p[t][0][2 * j + i] = pack_bf16(e[2 * i], e[2 * i + 1]);
           } else {
             uint32_t x[3], y[3];
             cut(__float_as_uint(e[2 * i]), x);
             cut(__float_as_uint(e[2 * i + 1]), y);
 #pragma unroll
-            for (int c = 0; c < 3; ++c) p[t][j / 2][c][2 * (j & 1) + i] = __builtin_amdgcn_perm(y[c], x[c], 0x07060302u);
+            for (int c = 0; c < 3; ++c) p[t][c][2 * j + i] = __builtin_amdgcn_perm(y[c], x[c], 0x07060302u);
           }
         }
       }
       l[t] += sum;
     }
+  }
+
+  template <bool MASKED>
+  __device__ __forceinline__ void values(const KvRegs<FMT, D> (&r)[KT], int base, uint32_t there, int n_keys, int g) {
+    uint32_t keep[4];                            // tokens past the end hold anything: cleared
+    if constexpr (MASKED) {
 #pragma unroll
-    for (int a = 0; a < KT / 2; ++a) {
-      uint32_t keep[4];                          // tokens past the end hold anything: cleared
-      if constexpr (MASKED) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = 2 * a + i / 2, key = base + 16 * j + 4 * g + 2 * (i & 1);
-          const bool on = (there >> j) & 1;
-          keep[i] = (on && key < n_keys ? 0xFFFFu : 0u) | (on && key + 1 < n_keys ? 0xFFFF0000u : 0u);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int j = i / 2, key = base + 16 * j + 4 * g + 2 * (i & 1);
+        const bool on = (there >> j) & 1;
+        keep[i] = (on && key < n_keys ? 0xFFFFu : 0u) | (on && key + 1 < n_keys ? 0xFFFF0000u : 0u);
       }
+    }
 #pragma unroll
-      for (int sg = 0; sg < L::NSEG; ++sg) {
-        constexpr int P4 = 2 * L::DPB;           // pairs of a dword
-        const int pairs = L::lane(sg) / 2;       // pairs of a lane and token
-        float sc[2][4];
+    for (int sg = 0; sg < L::NSEG; ++sg) {
+      constexpr int P4 = 2 * L::DPB;             // pairs of a dword
+      const int pairs = L::lane(sg) / 2;         // pairs of a lane and token
+      float sc[KT][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < KT; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[x][i] = kv_scale((r[2 * a + x].vs[sg] >> (8 * i)) & 255u);
+        for (int i = 0; i < 4; ++i) sc[x][i] = kv_scale((r[x].vs[sg] >> (8 * i)) & 255u);
 #pragma unroll
-        for (int pr = 0; pr < pairs; ++pr) {
-          u32x4 v[2];
+      for (int pr = 0; pr < pairs; ++pr) {
+        u32x4 v[2];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t w[4];
+        for (int x = 0; x < KT; ++x) {
+          uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = i * pairs + pr;     // the pair's place in the lane's codes
-              w[i] = kv_pair<FMT>(r[2 * a + x].v[L::off(sg) / 16 + at / P4], sc[x][i], at % P4);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              v[h][2 * x] = zip(w[0], w[1], h);
-              v[h][2 * x + 1] = zip(w[2], w[3], h);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int at = i * pairs + pr;       // the pair's place in the lane's codes
+            w[i] = kv_pair<FMT>(r[x].v[L::off(sg) / 16 + at / P4], sc[x][i], at % P4);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int d = L::dim0(sg) / 16 + 2 * pr + h;
-            if constexpr (MASKED) {
-              u32x4 nf;
+            v[h][2 * x] = zip(w[0], w[1], h);
+            v[h][2 * x + 1] = zip(w[2], w[3], h);
+          }
+        }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                v[h][i] &= keep[i];
-                nf[i] = not_finite16(v[h][i]);
-              }
-              // 0 times NaN is NaN: a value that is not finite must reach the rows that see it only.
-              // It counts as 0 here, and rows whose seen keys hold one get NaN.
-              if (__ballot((nf[0] | nf[1] | nf[2] | nf[3]) != 0)) {
+        for (int h = 0; h < 2; ++h) {
+          const int d = L::dim0(sg) / 16 + 2 * pr + h;
+          if constexpr (MASKED) {
+            u32x4 nf;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[h][i] &= ~whole16(nf[i]);
+            for (int i = 0; i < 4; ++i) {
+              v[h][i] &= keep[i];
+              nf[i] = not_finite16(v[h][i]);
+            }
+            // 0 times NaN is NaN: a value that is not finite must reach the rows that see it only.
+            // It counts as 0 here, and rows whose seen keys hold one get NaN.
+            if (__ballot((nf[0] | nf[1] | nf[2] | nf[3]) != 0)) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                  u32x4 vis;
+              for (int i = 0; i < 4; ++i) v[h][i] &= ~whole16(nf[i]);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const int j = 2 * a + i / 2, key = base + 16 * j + 4 * g + 2 * (i & 1);
-                    vis[i] = (key >= begin[t] && key < end[t] ? 0x3F80u : 0u) |
-                             (key + 1 >= begin[t] && key + 1 < end[t] ? 0x3F800000u : 0u);
-                  }
-                  const f32x4_t hit = mfma16(nf, vis, f32x4_t{0, 0, 0, 0});
+              for (int t = 0; t < NT; ++t) {
+                u32x4 vis;
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) o[t][d][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[t][d][i];
+                for (int i = 0; i < 4; ++i) {
+                  const int key = base + 16 * (i / 2) + 4 * g + 2 * (i & 1);
+                  vis[i] = (key >= begin[t] && key < end[t] ? 0x3F80u : 0u) |
+                           (key + 1 >= begin[t] && key + 1 < end[t] ? 0x3F800000u : 0u);
                 }
+                const f32x4_t hit = mfma16(nf, vis, f32x4_t{0, 0, 0, 0});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[t][d][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[t][d][i];
               }
             }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int c = PP - 1; c >= 0; --c) o[t][d] = mfma16(v[h], p[t][a][c], o[t][d]);
           }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = QP - 1; c >= 0; --c) o[t][d] = mfma16(v[h], p[t][c], o[t][d]);
         }
       }
     }
@@ -410,8 +423,14 @@ __device__ __forceinline__ void kv_store(const KvAttn& a, const KvSpan& sp, int 
   }
 }
 
+// Waves of a SIMD to compile for.
+constexpr int few_waves_simd(int dtype, int dim, int nt) {
+  const int need = (dtype == NC_BF16 ? 1 : 3) * nt * dim / 8 + nt * dim / 4 + 97;
+  return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
+}
+
 template <int FMT, int D, int DT, int NT, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES) kv_few(KvAttn a) {
+__global__ void __launch_bounds__(64 * WAVES, few_waves_simd(DT, D, NT)) kv_few(KvAttn a) {
   using L = Kv<FMT, D>;
   using F = Few<FMT, D, DT, NT>;
   constexpr int KT = F::KT;
@@ -436,6 +455,9 @@ __global__ void __launch_bounds__(64 * WAVES) kv_few(KvAttn a) {
   const int t0 = any_begin / 16 + chunk * a.chunk;
   const int t1 = min((any_end + 15) >> 4, t0 + a.chunk);
 
+  // a negative scale is the negated query's
+  const float scale2 = fabsf(a.scale2);
+  const uint32_t flip = a.scale2 < 0 ? 0x80008000u : 0u;
   F f;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -454,46 +476,65 @@ __global__ void __launch_bounds__(64 * WAVES) kv_few(KvAttn a) {
 #pragma unroll
       for (int st = 0; st < L::piece(sg) / 8; ++st)
         load_q<DT>(f.q[t][L::dim0(sg) / 32 + st], a.q.p, at + L::dim0(sg) + g * L::piece(sg) + 8 * st, live);
+#pragma unroll
+    for (int st = 0; st < D / 32; ++st)
+#pragma unroll
+      for (int c = 0; c < F::QP; ++c) f.q[t][st][c] ^= flip;
   }
 
-  // Steps of KT tiles, the waves in turn.  Lane i looks up the i-th tile that
-  // the wave takes, 64 tiles at a time.
-  constexpr int STRIDE = KT * WAVES;
-  int ids = -1;
-  KvRegs<FMT, D> next[KT];
-  uint32_t there = 0;
-  auto look_up = [&](int k) {                    // k: the wave's next step
-    const int t = t0 + (k + lane / KT) * STRIDE + wave * KT + lane % KT;
-    ids = t < t1 ? kv_tile_at(a, b, h, t) : -1;
-  };
-  auto fetch = [&](int k) {
-    there = 0;
+  // Steps of KT tiles, the waves in turn, 64 / KT steps at a time: lane i looks up the i-th tile
+  // that the wave takes in them.  Steps without masks come first (the order does not matter to the
+  // sums), then those that some row sees in part or that lack a page.  A step's keys and values are
+  // loaded as soon as the step before has used its own.
+  constexpr int STRIDE = KT * WAVES, BATCH = 64 / KT;
+  const int w0 = t0 + wave * KT;                 // the wave's first tile
+  const int steps = w0 < t1 ? (t1 - w0 + STRIDE - 1) / STRIDE : 0;
+  for (int k0 = 0; k0 < steps; k0 += BATCH) {
+    const int n = min(steps - k0, BATCH);
+    const int t = w0 + (k0 + lane / KT) * STRIDE + lane % KT;
+    const bool mine = lane < n * KT && t < t1;
+    const int ids = mine ? kv_tile_at(a, b, h, t) : -1;
+    // plain steps of the batch: [ka, kb)
+    const int at0 = 16 * (w0 + k0 * STRIDE);
+    int ka = all_begin > at0 ? (all_begin - at0 + 16 * STRIDE - 1) / (16 * STRIDE) : 0;
+    const int whole = min(all_end, 16 * t1);
+    int kb = whole >= at0 + 16 * KT ? (whole - at0 - 16 * KT) / (16 * STRIDE) + 1 : 0;
+    kb = min(kb, n);
+    if (kb <= ka || __ballot(mine && ids < 0)) ka = kb = 0;
+    KvRegs<FMT, D> r[KT];
+    auto tile = [&](int k, int j) {
+      return a.cache.data + (int64_t)max(__builtin_amdgcn_readlane(ids, (k * KT + j) & 63), 0) * L::TILE;
+    };
+    auto keys = [&](int k) {
 #pragma unroll
-    for (int j = 0; j < KT; ++j) {
-      const int tile = __builtin_amdgcn_readlane(ids, (k % (64 / KT)) * KT + j);
-      there |= tile >= 0 ? 1u << j : 0u;
-      load_tile<FMT, D>(next[j], a.cache.data + (int64_t)max(tile, 0) * L::TILE, m, g);
-    }
-  };
-  const int mine = t1 - t0 - wave * KT;          // tiles from the wave's first on
-  const int steps = mine > 0 ? (mine + STRIDE - 1) / STRIDE : 0;
-  if (steps > 0) {
-    look_up(0);
-    fetch(0);
-    for (int k = 0; k < steps; ++k) {
-      KvRegs<FMT, D> now[KT];
+      for (int j = 0; j < KT; ++j) load_keys<FMT, D>(r[j], tile(k, j), m, g);
+    };
+    auto vals = [&](int k) {
 #pragma unroll
-      for (int j = 0; j < KT; ++j) now[j] = next[j];
-      const uint32_t have = there;
-      if (k + 1 < steps) {
-        if ((k + 1) % (64 / KT) == 0) look_up(k + 1);
-        fetch(k + 1);
+      for (int j = 0; j < KT; ++j) load_values<FMT, D>(r[j], tile(k, j), m, g);
+    };
+    if (ka < kb) {
+      keys(ka);
+      vals(ka);
+      for (int k = ka; k < kb; ++k) {
+        const int next = k + 1 < kb ? k + 1 : k;
+        f.scores(r);
+        keys(next);
+        f.template weights<false>(0, 0, scale2, g);
+        f.template values<false>(r, 0, 0, 0, g);
+        vals(next);
       }
-      const int base = (t0 + k * STRIDE + wave * KT) * 16;
-      if (have == (1u << KT) - 1 && base >= all_begin && base + 16 * KT <= all_end)
-        f.template step<false>(now, base, have, sp.n, a.scale2, g);
-      else
-        f.template step<true>(now, base, have, sp.n, a.scale2, g);
+    }
+    for (int k = ka > 0 ? 0 : kb; k < n; k = k + 1 == ka ? kb : k + 1) {
+      uint32_t there = 0;
+#pragma unroll
+      for (int j = 0; j < KT; ++j) there |= __builtin_amdgcn_readlane(ids, k * KT + j) >= 0 ? 1u << j : 0u;
+      const int base = at0 + 16 * STRIDE * k;
+      keys(k);
+      vals(k);
+      f.scores(r);
+      f.template weights<true>(base, there, scale2, g);
+      f.template values<true>(r, base, there, sp.n, g);
     }
   }
 
@@ -553,9 +594,8 @@ hipError_t few_launch(const KvAttn& a, hipStream_t stream) {
 template <int FMT, int D, int DT>
 hipError_t few_by_rows(const KvAttn& a, const KvPlan& p, hipStream_t stream) {
   if (p.rows == 16) return few_launch<FMT, D, DT, 1, kKvFewWaves>(a, stream);
-  if (p.rows == 32) return few_launch<FMT, D, DT, 2, kKvFewWaves>(a, stream);
-  if constexpr (kv_few_rows_most(DT, D) == 64)
-    if (p.rows == 64) return few_launch<FMT, D, DT, 4, kKvFewWaves>(a, stream);
+  if constexpr (kv_few_rows(DT, D) == 32)
+    if (p.rows == 32) return few_launch<FMT, D, DT, 2, kKvFewWaves>(a, stream);
   return hipErrorInvalidValue;
 }
 

@@ -14,10 +14,6 @@
 // lane (and its partner 32 lanes on) in the order the second product wants
 // them.  Two LDS buffers: a step's conversion goes beside the products of the
 // step before, with one barrier between steps.
-//
-// The running reference m of a row follows its maximum only when that has
-// grown by more than 2^8: weights then stay below 2^8 and the sums are
-// rescaled a few times per call instead of at every new maximum.
 #pragma once
 
 #include "nc_kv_few.h"
@@ -31,7 +27,6 @@ __device__ __forceinline__ f32x16_t mfma32(const u32x4& a, const u32x4& b, const
 }
 
 constexpr int kManyWaves = 4, kManyKeys = 64;
-constexpr float kManyGrowth = 8.0f;
 
 template <int FMT, int D> struct ManyLds {
   uint32_t k[D / 8][kManyKeys][4];
@@ -142,7 +137,7 @@ template <int FMT, int D, int DT> struct Many {
     }
     top = max_halves(top) * scale2;
     if (MASKED && !(top > -INFINITY)) top = -INFINITY;       // 0 scale times no key
-    if (__ballot(top > m + kManyGrowth)) {
+    if (__ballot(top > m + kGrowth)) {
       const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
       l *= f;
 #pragma unroll
@@ -295,7 +290,9 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   auto fetch = [&](int k) {                      // past the last step: the cache's first tile, unused
     const int tile = __builtin_amdgcn_readlane(ids, k & 63);
     there = tile >= 0;
-    load_tile<FMT, D>(next, a.cache.data + (int64_t)max(tile, 0) * L::TILE, lane & 15, lane >> 4);
+    const uint8_t* p = a.cache.data + (int64_t)max(tile, 0) * L::TILE;
+    load_keys<FMT, D>(next, p, lane & 15, lane >> 4);
+    load_values<FMT, D>(next, p, lane & 15, lane >> 4);
   };
   auto put = [&](int k) {
     if (k >= ka && k < kb) {

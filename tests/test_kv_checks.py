@@ -180,11 +180,11 @@ def test_binding_write_and_read():
             call(c, bf16(4, 2, 64), bf16(5, 2, 64), s)
         with pytest.raises(ValueError, match="v: shape"):
             call(c, bf16(5, 2, 64), bf16(5, 3, 64), s)
-        with pytest.raises(ValueError, match="v: dtype"):
+        with pytest.raises(ValueError, match="v: .*float32"):
             call(c, bf16(5, 2, 64), bf16(5, 2, 64).float(), s)
         with pytest.raises(TypeError):
             call(c, bf16(5, 2, 64).half(), bf16(5, 2, 64).half(), s)
-        with pytest.raises(ValueError, match="slots: dtype"):
+        with pytest.raises(ValueError, match="slots: .*int32"):
             call(c, bf16(5, 2, 64), bf16(5, 2, 64), s.int())
         with pytest.raises(ValueError, match="slots: shape"):
             call(c, bf16(5, 2, 64), bf16(5, 2, 64), s[:, None])
@@ -209,7 +209,7 @@ def test_binding_attention():
         call()
     for kw, match in ((dict(q=bf16(3, 3, 64)), "q: 3 heads"), (dict(q=bf16(3, 4, 96)), "q: shape"),
                       (dict(q=bf16(12, 64)), "q: shape"), (dict(out=bf16(2, 4, 64)), "out: shape"),
-                      (dict(out=bf16(3, 4, 64).float()), "out: dtype"), (dict(out=bf16(3, 1, 64).expand(3, 4, 64)), "overlap"),
+                      (dict(out=bf16(3, 4, 64).float()), "out: .*float32"), (dict(out=bf16(3, 1, 64).expand(3, 4, 64)), "overlap"),
                       (dict(q_start=i32(0, 3)), "q_start"), (dict(q_start=torch.tensor([0, 1, 3])), "q_start: .*int64"),
                       (dict(kv_len=torch.tensor([9, 9])), "kv_len: .*int64"), (dict(table=torch.zeros((2, 2))), "table: shape"),
                       (dict(table=torch.zeros((3, 2), dtype=torch.int32)), "table: shape"),
