@@ -101,33 +101,35 @@ struct KvAttn {
   int32_t group;           // query heads of a cache head
   int32_t causal, window;  // window 0: none
   float scale2;            // score scale times log2(e)
-  // the split: each workgroup takes `rows` rows (query, head of the group) of
-  // one sequence and cache head and `chunk` tiles of keys
-  int32_t row_groups, chunk, chunks;
-  float* part;             // partial results, chunks > 1 only
+  // the split: workgroups take row groups of one sequence and cache head.  Few rows:
+  // `shares` workgroups with equal shares of all tiles (0: one for each row group);
+  // many rows: `chunks` workgroups of `chunk` tiles
+  int32_t row_groups, shares, chunk, chunks;
+  float* part;             // partial results
 };
 
 // What the split of a call is, from its sizes (host): shared by the workspace
 // size and the launch.
 struct KvPlan {
-  int32_t rows;         // rows of a workgroup
+  int32_t rows;         // rows of a workgroup: 16 or 32 (few), kKvManyRows
   int32_t row_groups;   // workgroups along the rows of one (sequence, head)
-  int32_t chunk;        // tiles of 16 keys of a workgroup
-  int32_t chunks;       // workgroups along the keys, at most `most`
+  int32_t shares;       // few: equal shares of the tiles, 0 for a workgroup to a row group
+  int32_t chunk;        // many: tiles of 16 keys of a workgroup
+  int32_t chunks;       // many: workgroups along the keys, at most `most`
   int32_t most;         // does not fall as the span of keys grows
 };
 
 constexpr int kKvFewWaves = 4;
+constexpr int kKvShareLeast = 16;  // fewest tiles of a share
 constexpr int kKvManyRows = 128;   // rows of a workgroup of the many-row kernel
 // Most rows of a workgroup of the few-row kernel: 32 where their queries and sums fit the registers.
 constexpr int kv_few_rows(int dtype, int dim) { return dtype == NC_BF16 || dim <= 128 ? 32 : 16; }
 
 // Rows (query i of the sequence, head j of the group) are numbered i * group + j.
-// Partial results of chunk c, sequence b, head h, row r: D unnormalised sums, at
-// ((b * heads + h) * chunks + c) * rows_all + r, then the running maximum and sum.
-inline size_t kv_part_bytes(int64_t batch, int64_t heads, int64_t chunks, int64_t rows_all, int dim) {
-  return chunks > 1 ? (size_t)(batch * heads * chunks * rows_all) * (size_t)(dim + 2) * 4 : 0;
-}
+// Partial results: places of D unnormalised sums, then a maximum and a sum for
+// each place.  Many rows: place ((b * heads + h) * chunks + c) * rows_all + r;
+// few rows: two for each share and row of a group.
+inline size_t kv_part_bytes(int64_t places, int dim) { return (size_t)places * (size_t)(dim + 2) * 4; }
 
 hipError_t launch_kv_write(const KvCache& c, int fmt, int dim, const KvRows<const void*>& k, const KvRows<const void*>& v,
                            int dtype, const int64_t* slots, int64_t tokens, int rule, hipStream_t stream);
@@ -141,6 +143,6 @@ hipError_t kv_many_e2m1_bf16(const KvAttn& a, int dim, hipStream_t stream);
 hipError_t kv_many_e2m1_f32(const KvAttn& a, int dim, hipStream_t stream);
 hipError_t kv_many_e4m3_bf16(const KvAttn& a, int dim, hipStream_t stream);
 hipError_t kv_many_e4m3_f32(const KvAttn& a, int dim, hipStream_t stream);
-hipError_t launch_kv_join(const KvAttn& a, int dim, int dtype, hipStream_t stream);
+hipError_t launch_kv_join(const KvAttn& a, int dim, int dtype, const KvPlan& p, hipStream_t stream);
 
 }  // namespace nc

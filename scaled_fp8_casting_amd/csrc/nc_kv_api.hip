@@ -52,18 +52,28 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
 
 // The split of a call.  span: tiles of 16 keys that a row group may reach.
 KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_t rows_all, int64_t span) {
-  KvPlan p;
+  KvPlan p = {};
   const bool many = rows_all > 32;
   p.rows = many ? kKvManyRows : (rows_all <= 16 ? 16 : kv_few_rows(dtype, dim));
   p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
   const int64_t base = std::max<int64_t>(1, batch * heads * p.row_groups);
-  // few rows: at least 32 tiles (512 keys) each, at most about 1024 workgroups; many: 16 tiles, 512 workgroups
-  const int64_t want = many ? std::min<int64_t>(512 / base, span / 16) : std::min<int64_t>((1024 + base - 1) / base, span / 32);
-  const int64_t chunks = std::max<int64_t>(1, want);
-  p.most = (int32_t)chunks;
-  p.chunk = (int32_t)std::max<int64_t>(1, (span + chunks - 1) / chunks);
-  p.chunks = (int32_t)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
+  p.chunks = p.most = 1;
+  p.chunk = (int32_t)std::max<int64_t>(1, span);
+  if (many) {
+    // at least 16 tiles each, at most about 512 workgroups
+    p.most = (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / base, span / 16));
+    p.chunk = (int32_t)std::max<int64_t>(1, (span + p.most - 1) / p.most);
+    p.chunks = (int32_t)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
+  } else if (span > 64) {
+    p.shares = (int32_t)std::min<int64_t>(768, (base * span + kKvShareLeast - 1) / kKvShareLeast);
+  }
   return p;
+}
+
+// Partial places of a call, those of any shorter span included.
+int64_t places_of(const KvPlan& p, int64_t batch, int64_t heads, int64_t rows_all) {
+  if (p.shares > 0) return 2 * (int64_t)p.shares * p.rows;
+  return p.most > 1 ? batch * heads * p.most * rows_all : 0;
 }
 
 int64_t span_of(int64_t max_kv, int64_t max_q, int64_t window) {
@@ -115,7 +125,7 @@ size_t nc_kv_workspace_bytes(const nc_kv_cache* c, nc_dtype dtype, int32_t q_hea
   const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
   // a window only shortens the span, and a shorter span never raises the most
   const KvPlan p = plan_of(c->dim, dtype, batch, c->heads, rows, span_of(max_kv, max_q, 0) + 1);
-  return kv_part_bytes(batch, c->heads, p.most, rows, c->dim);
+  return kv_part_bytes(places_of(p, batch, c->heads, rows), c->dim);
 }
 
 nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dtype, void* ws, size_t ws_bytes,
@@ -154,14 +164,16 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   const int64_t rows = (int64_t)a->max_q * k.group;
   const KvPlan p = plan_of(c->dim, dtype, a->batch, c->heads, rows, span_of(a->max_kv, a->max_q, a->window));
   k.row_groups = p.row_groups;
+  k.shares = p.shares;
   k.chunk = p.chunk;
   k.chunks = p.chunks;
   k.part = (float*)ws;
-  if ((int64_t)a->batch * c->heads * p.row_groups * p.chunks > INT32_MAX) return NC_E_ARG;
-  if (p.chunks > 1) {
-    if (ws == nullptr || !aligned16(ws) || ws_bytes < kv_part_bytes(a->batch, c->heads, p.chunks, rows, c->dim))
-      return NC_E_WORKSPACE;
-  }
+  const int64_t span = span_of(a->max_kv, a->max_q, a->window);
+  if ((int64_t)a->batch * c->heads * p.row_groups * std::max<int64_t>(p.chunks, span + 1) > INT32_MAX) return NC_E_ARG;
+  const bool split = p.shares > 0 || p.chunks > 1;
+  if (split && (ws == nullptr || !aligned16(ws) ||
+                ws_bytes < kv_part_bytes(places_of(p, a->batch, c->heads, rows), c->dim)))
+    return NC_E_WORKSPACE;
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e;
   const bool b16 = dtype == NC_BF16;
@@ -172,7 +184,7 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
     if (c->fmt == NC_E2M1) e = b16 ? kv_few_e2m1_bf16(k, c->dim, p, st) : kv_few_e2m1_f32(k, c->dim, p, st);
     else e = b16 ? kv_few_e4m3_bf16(k, c->dim, p, st) : kv_few_e4m3_f32(k, c->dim, p, st);
   }
-  if (e == hipSuccess && p.chunks > 1) e = launch_kv_join(k, c->dim, dtype, st);
+  if (e == hipSuccess && split) e = launch_kv_join(k, c->dim, dtype, p, st);
   return hip_status(e);
 }
 

@@ -403,57 +403,111 @@ template <int FMT, int D, int DT, int NT> struct Few {
   }
 };
 
-// Four elements of a row: the call's result when the row's keys are one chunk,
-// else partial sums.  A chunk in which the row sees nothing leaves its sums
-// unwritten; its maximum says so.
+// Where a workgroup's sums of a row go: the call's result, or a place among the
+// partial results (D sums; maximum and sum in a list behind all of them).
 template <int DT>
-__device__ __forceinline__ void kv_store(const KvAttn& a, const KvSpan& sp, int b, int h, int chunk, int r, int rows_all,
-                                         int dim, int c, const f32x4_t& o, float top, float sum) {
-  if (a.chunks == 1) {
+__device__ __forceinline__ void kv_store(const KvAttn& a, const KvSpan& sp, int h, int r, int dim, int c, const f32x4_t& o,
+                                         float top, float sum, int64_t place, int64_t places) {
+  if (place < 0) {
     kv_result<DT>(a, sp, h, r, c, o, top, sum);
     return;
   }
-  const int64_t n = (int64_t)a.batch * a.cache.heads * a.chunks * rows_all;
-  const int64_t at = ((int64_t)(b * a.cache.heads + h) * a.chunks + chunk) * rows_all + r;
-  if (top != -INFINITY || sum != 0.0f) *reinterpret_cast<f32x4_t*>(a.part + at * dim + c) = o;
+  *reinterpret_cast<f32x4_t*>(a.part + place * dim + c) = o;
   if (c == 0) {
-    float* ml = a.part + n * dim + at * 2;
+    float* ml = a.part + places * dim + place * 2;
     ml[0] = top;
     ml[1] = sum;
   }
 }
 
+// ---- how the few-row kernel's work is shared out ----------------------------
+// A segment is one (sequence, head, row group); its length is the tiles of 16
+// keys that the sequence's rows reach, at least 1.  Lengths live on the device,
+// so each workgroup works them out: all segments lie one after the other on a
+// line, and workgroup w takes the tiles [w share, (w + 1) share) of it, however
+// unequal the sequences are.  Whole segments inside a share are finished there;
+// the one that began before it goes to partial place 2 w, the one that goes on
+// behind it to place 2 w + 1.
+struct KvReach {
+  KvSpan sp;
+  int t0, tiles;       // first tile, tiles of a segment (0: no queries)
+};
+__device__ __forceinline__ KvReach kv_reach(const KvAttn& a, int b) {
+  KvReach r;
+  r.sp = kv_span(a, b);
+  const int end = kv_end(a, r.sp, r.sp.q_len - 1);
+  r.t0 = kv_begin(a, kv_end(a, r.sp, 0)) / 16;
+  r.tiles = r.sp.q_len > 0 ? max(1, (end + 15) / 16 - r.t0) : 0;
+  return r;
+}
+// The same for a sequence that is the whole wave's.
+__device__ __forceinline__ KvReach kv_reach_wave(const KvAttn& a, int b) {
+  const KvReach r = kv_reach(a, b);
+  const auto u = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  return KvReach{{u(r.sp.n), u(r.sp.q_len), u(r.sp.q0)}, u(r.t0), u(r.tiles)};
+}
+__device__ __forceinline__ uint32_t scan64(uint32_t x, int lane) {   // inclusive sum over the wave
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t y = __shfl_up(x, d);
+    x += lane >= d ? y : 0u;
+  }
+  return x;
+}
+// Tiles of all segments; with 64 sequences at most `mine` is lane i's sequence's share of them.
+__device__ __forceinline__ uint32_t kv_line(const KvAttn& a, int lane) {
+  uint32_t sum = 0;
+  for (int b = lane; b < a.batch; b += 64) sum += (uint32_t)kv_reach(a, b).tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+  return sum * (uint32_t)(a.cache.heads * a.row_groups);
+}
+// The sequence that holds tile x of the line, and where it begins.
+__device__ __forceinline__ int kv_find(const KvAttn& a, uint32_t x, int lane, uint32_t& start) {
+  const uint32_t per = (uint32_t)(a.cache.heads * a.row_groups);
+  uint32_t before = 0;
+  for (int b = 0; b < a.batch; b += 64) {
+    const uint32_t n = b + lane < a.batch ? (uint32_t)kv_reach(a, b + lane).tiles * per : 0u;
+    const uint32_t to = before + scan64(n, lane);
+    const uint64_t past = __ballot(to > x);
+    if (past) {
+      const int i = __builtin_ctzll(past);
+      start = __builtin_amdgcn_readlane(to - n, i);
+      return b + i;
+    }
+    before = __builtin_amdgcn_readlane(to, 63);
+  }
+  start = before;
+  return a.batch;
+}
+__device__ __forceinline__ uint32_t kv_share(const KvAttn& a, uint32_t line) {
+  const uint32_t n = (line + (uint32_t)a.shares - 1) / (uint32_t)a.shares;
+  return max((n + 7) & ~7u, (uint32_t)kKvShareLeast);
+}
+
 // Waves of a SIMD to compile for.
 constexpr int few_waves_simd(int dtype, int dim, int nt) {
-  const int need = (dtype == NC_BF16 ? 1 : 3) * nt * dim / 8 + nt * dim / 4 + 97;
+  const int need = (dtype == NC_BF16 ? 1 : 3) * nt * dim / 8 + nt * dim / 4 + 110;
   return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
 }
 
+// One segment's tiles [t0, t1): the workgroup's sums into the result (place < 0)
+// or a partial place.
 template <int FMT, int D, int DT, int NT, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, few_waves_simd(DT, D, NT)) kv_few(KvAttn a) {
+__device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, int b, int h, int rg, int t0, int t1, int place,
+                                            float* lds) {
   using L = Kv<FMT, D>;
   using F = Few<FMT, D, DT, NT>;
   constexpr int KT = F::KT;
-  // one row tile's sums of every wave, then every row's maximum and sum
-  __shared__ __align__(16) float lds[WAVES * 16 * (D + 4) + WAVES * 16 * NT * 2];
+  const int64_t places = 2 * (int64_t)a.shares * 16 * NT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
-  // workgroup -> chunk of keys, row group, head, sequence
-  uint32_t id = blockIdx.x;
-  const int chunk = id % a.chunks;
-  id /= a.chunks;
-  const int rg = id % a.row_groups;
-  id /= a.row_groups;
-  const int h = id % a.cache.heads, b = id / a.cache.heads;
-  const KvSpan sp = kv_span(a, b);
-  const int rows_all = a.max_q * a.group, rows = sp.q_len * a.group, row0 = rg * 16 * NT;
+  const int rows = sp.q_len * a.group, row0 = rg * 16 * NT;
   if (row0 >= rows) return;
   const int i_lo = row0 / a.group, i_hi = (min(rows, row0 + 16 * NT) - 1) / a.group;
   // keys that some row sees, and keys that every row sees
-  const int any_end = kv_end(a, sp, i_hi), all_end = kv_end(a, sp, i_lo);
-  const int any_begin = kv_begin(a, all_end), all_begin = kv_begin(a, any_end);
-  const int t0 = any_begin / 16 + chunk * a.chunk;
-  const int t1 = min((any_end + 15) >> 4, t0 + a.chunk);
+  const int any_end = kv_end(a, sp, i_hi), all_end = kv_end(a, sp, i_lo), all_begin = kv_begin(a, any_end);
+  t1 = min(t1, (any_end + 15) >> 4);
 
   // a negative scale is the negated query's
   const float scale2 = fabsf(a.scale2);
@@ -579,14 +633,57 @@ __global__ void __launch_bounds__(64 * WAVES, few_waves_simd(DT, D, NT)) kv_few(
         sum += x * ml[(w * NT * 16 + t * 16 + rr) * 2 + 1];
         o += x * *reinterpret_cast<const f32x4_t*>(lds + (w * 16 + rr) * (D + 4) + c);
       }
-      kv_store<DT>(a, sp, b, h, chunk, r, rows_all, D, c, o, top, sum);
+      kv_store<DT>(a, sp, h, r, D, c, o, top, sum, place < 0 ? place : place * (16 * NT) + 16 * t + rr, places);
     }
+  }
+}
+
+
+template <int FMT, int D, int DT, int NT, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, few_waves_simd(DT, D, NT)) kv_few(KvAttn a) {
+  // one row tile's sums of every wave, then every row's maximum and sum
+  __shared__ __align__(16) float lds[WAVES * 16 * (D + 4) + WAVES * 16 * NT * 2];
+  const uint32_t per = (uint32_t)(a.cache.heads * a.row_groups);
+  uint32_t x, to, start = 0, seg;                // tiles [x, to) of the line; segment seg of sequence b begins at start
+  int b;
+  KvReach r;
+  if (a.shares == 0) {                           // a workgroup for each segment
+    b = blockIdx.x / per;
+    seg = blockIdx.x - (uint32_t)b * per;
+    r = kv_reach_wave(a, b);
+    x = 0;
+    to = (uint32_t)r.tiles;
+    if (to == 0) return;
+  } else {
+    const int lane = threadIdx.x & 63;
+    const uint32_t line = __builtin_amdgcn_readfirstlane(kv_line(a, lane)), share = kv_share(a, line);
+    x = blockIdx.x * share;
+    to = min(line, x + share);
+    if (x >= to) return;
+    b = __builtin_amdgcn_readfirstlane(kv_find(a, x, lane, start));
+    r = kv_reach_wave(a, b);
+    seg = (x - start) / (uint32_t)r.tiles;
+    start += seg * (uint32_t)r.tiles;
+  }
+  for (;;) {
+    const uint32_t end = start + (uint32_t)r.tiles, stop = min(end, to);
+    const int rg = seg % (uint32_t)a.row_groups, h = seg / (uint32_t)a.row_groups;
+    const int place = x == start && stop == end ? -1 : 2 * (int)blockIdx.x + (x == start ? 1 : 0);
+    few_segment<FMT, D, DT, NT, WAVES>(a, r.sp, b, h, rg, r.t0 + (int)(x - start), r.t0 + (int)(stop - start), place, lds);
+    x = start = stop;
+    if (x >= to) return;
+    if (++seg == per) {
+      seg = 0;
+      do r = kv_reach_wave(a, ++b);                   // ends: x is inside the line
+      while (r.tiles == 0);
+    }
+    __syncthreads();                             // before the sums in LDS are overwritten
   }
 }
 
 template <int FMT, int D, int DT, int NT, int WAVES>
 hipError_t few_launch(const KvAttn& a, hipStream_t stream) {
-  const int64_t grid = (int64_t)a.batch * a.cache.heads * a.row_groups * a.chunks;
+  const int64_t grid = a.shares > 0 ? a.shares : (int64_t)a.batch * a.cache.heads * a.row_groups;
   kv_few<FMT, D, DT, NT, WAVES><<<dim3((uint32_t)grid), dim3(64 * WAVES), 0, stream>>>(a);
   return hipGetLastError();
 }

@@ -1,32 +1,33 @@
-// Joining the partial results of attention chunks: out = sum_c 2^(m_c - m) o_c
-// / sum_c 2^(m_c - m) l_c in a fixed order.  A workgroup takes one row; its
-// threads are D / 4 columns of four elements times P lines of chunks, each
-// line in one pass with a running maximum, the lines joined in LDS.
+// Joining partial results: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c
+// in a fixed order.  A workgroup takes one row; its threads are D / 4 columns
+// of four elements times P lines of partial results, the lines joined in LDS.
 #include "nc_kv_few.h"
 
 namespace nc {
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
+
+// Places first, first + 1 * step, ... of a row, n of them; `head` is the first
+// place (it may lie off the run).
+struct KvParts {
+  int64_t head, first, step, places;
+  int n;
+};
 
 template <int D, int DT>
-__global__ void __launch_bounds__(kJoinThreads) kv_join(KvAttn a) {
+__device__ __forceinline__ void join_row(const KvAttn& a, const KvSpan& sp, int h, int r, const KvParts& p) {
   constexpr int COLS = D / 4, P = kJoinThreads / COLS;
   __shared__ __align__(16) float lds[P * (D + 2)];
-  const int rows_all = a.max_q * a.group;
-  const uint32_t r = blockIdx.x % (uint32_t)rows_all, bh = blockIdx.x / (uint32_t)rows_all;
-  const int h = bh % a.cache.heads, b = bh / a.cache.heads;
-  const KvSpan sp = kv_span(a, b);
-  if ((int)r >= sp.q_len * a.group) return;
   const int col = threadIdx.x % COLS, line = threadIdx.x / COLS;
-  const int64_t n = (int64_t)a.batch * a.cache.heads * a.chunks * rows_all;
+  const float* ml = a.part + p.places * D;
   float top = -INFINITY, sum = 0;
   f32x4_t o = {0, 0, 0, 0};
   if (line < P) {
-    for (int c = line; c < a.chunks; c += P) {
-      const int64_t at = ((int64_t)bh * a.chunks + c) * rows_all + r;
-      const float mc = a.part[n * D + at * 2], lc = a.part[n * D + at * 2 + 1];
-      if (mc == -INFINITY && lc == 0.0f) continue;     // nothing seen there
+#pragma unroll 4
+    for (int c = line; c < p.n; c += P) {
+      const int64_t at = c == 0 ? p.head : p.first + (c - 1) * p.step;
+      const float mc = ml[at * 2], lc = ml[at * 2 + 1];
       const f32x4_t oc = *reinterpret_cast<const f32x4_t*>(a.part + at * D + 4 * col);
       const float mn = fmaxf(top, mc), ref = mn == -INFINITY ? 0.0f : mn;
       const float x = exp2_fast(top - ref), y = exp2_fast(mc - ref);
@@ -42,38 +43,93 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join(KvAttn a) {
   }
   __syncthreads();
   if (line != 0) return;
+  const int lines = min(P, p.n);
   top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < P; ++i) top = fmaxf(top, lds[P * D + 2 * i]);
+  for (int i = 0; i < lines; ++i) top = fmaxf(top, lds[P * D + 2 * i]);
   const float ref = top == -INFINITY ? 0.0f : top;
   sum = 0;
   o = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
+  for (int i = 0; i < lines; ++i) {
     const float x = exp2_fast(lds[P * D + 2 * i] - ref);
     sum += x * lds[P * D + 2 * i + 1];
     o += x * *reinterpret_cast<const f32x4_t*>(lds + i * D + 4 * col);
   }
-  kv_result<DT>(a, sp, h, (int)r, 4 * col, o, top, sum);
+  kv_result<DT>(a, sp, h, r, 4 * col, o, top, sum);
 }
 
-template <int D>
-hipError_t join(const KvAttn& a, int dtype, hipStream_t stream) {
+template <int D, int DT>
+__global__ void __launch_bounds__(kJoinThreads) kv_join(KvAttn a) {
+  const int rows_all = a.max_q * a.group;
+  const int r = (int)(blockIdx.x % (uint32_t)rows_all);
+  const uint32_t bh = blockIdx.x / (uint32_t)rows_all;
+  const int h = bh % (uint32_t)a.cache.heads, b = bh / (uint32_t)a.cache.heads;
+  const KvSpan sp = kv_span(a, b);
+  if (r >= sp.q_len * a.group) return;
+  KvParts p;
+  p.places = (int64_t)a.batch * a.cache.heads * a.chunks * rows_all;
+  p.head = (int64_t)bh * a.chunks * rows_all + r;
+  p.step = rows_all;
+  p.first = p.head + p.step;
+  p.n = a.chunks;
+  join_row<D, DT>(a, sp, h, r, p);
+}
+
+// The few-row kernel's shares: only segments that lie in more than one.
+template <int D, int DT>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_shares(KvAttn a, int rows) {
+  const int rows_all = a.max_q * a.group, lane = threadIdx.x & 63;
+  const int r = (int)(blockIdx.x % (uint32_t)rows_all);
+  const uint32_t bh = blockIdx.x / (uint32_t)rows_all;
+  const int h = bh % (uint32_t)a.cache.heads, b = bh / (uint32_t)a.cache.heads;
+  const KvReach reach = kv_reach(a, b);
+  if (r >= reach.sp.q_len * a.group) return;
+  // where the segment lies on the line
+  uint32_t all = 0, before = 0;
+  for (int i = lane; i < a.batch; i += 64) {
+    const uint32_t n = (uint32_t)kv_reach(a, i).tiles;
+    all += n;
+    before += i < b ? n : 0u;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    all += __shfl_xor(all, d);
+    before += __shfl_xor(before, d);
+  }
+  const uint32_t per = (uint32_t)(a.cache.heads * a.row_groups);
+  const uint32_t share = kv_share(a, all * per);
+  const uint32_t start = before * per + ((uint32_t)h * a.row_groups + (uint32_t)(r / rows)) * (uint32_t)reach.tiles;
+  const uint32_t g0 = start / share, g1 = (start + (uint32_t)reach.tiles - 1) / share;
+  if (g0 == g1) return;
+  KvParts p;
+  p.places = 2 * (int64_t)a.shares * rows;
+  p.head = (int64_t)(2 * g0 + 1) * rows + r % rows;
+  p.step = 2 * rows;
+  p.first = (int64_t)(2 * g0 + 2) * rows + r % rows;
+  p.n = (int)(g1 - g0) + 1;
+  join_row<D, DT>(a, reach.sp, h, r, p);
+}
+
+template <int D, int DT>
+hipError_t join(const KvAttn& a, const KvPlan& p, hipStream_t stream) {
   const dim3 grid((uint32_t)((int64_t)a.batch * a.cache.heads * a.max_q * a.group));
-  if (dtype == NC_BF16) kv_join<D, NC_BF16><<<grid, dim3(kJoinThreads), 0, stream>>>(a);
-  else kv_join<D, NC_F32><<<grid, dim3(kJoinThreads), 0, stream>>>(a);
+  if (p.shares > 0) kv_join_shares<D, DT><<<grid, dim3(kJoinThreads), 0, stream>>>(a, p.rows);
+  else kv_join<D, DT><<<grid, dim3(kJoinThreads), 0, stream>>>(a);
   return hipGetLastError();
+}
+template <int D>
+hipError_t join_by_dtype(const KvAttn& a, int dtype, const KvPlan& p, hipStream_t stream) {
+  return dtype == NC_BF16 ? join<D, NC_BF16>(a, p, stream) : join<D, NC_F32>(a, p, stream);
 }
 
 }  // namespace
 
-hipError_t launch_kv_join(const KvAttn& a, int dim, int dtype, hipStream_t stream) {
+hipError_t launch_kv_join(const KvAttn& a, int dim, int dtype, const KvPlan& p, hipStream_t stream) {
   switch (dim) {
-    case 64: return join<64>(a, dtype, stream);
-    case 96: return join<96>(a, dtype, stream);
-    case 128: return join<128>(a, dtype, stream);
-    case 192: return join<192>(a, dtype, stream);
-    case 256: return join<256>(a, dtype, stream);
+    case 64: return join_by_dtype<64>(a, dtype, p, stream);
+    case 96: return join_by_dtype<96>(a, dtype, p, stream);
+    case 128: return join_by_dtype<128>(a, dtype, p, stream);
+    case 192: return join_by_dtype<192>(a, dtype, p, stream);
+    case 256: return join_by_dtype<256>(a, dtype, p, stream);
   }
   return hipErrorInvalidValue;
 }

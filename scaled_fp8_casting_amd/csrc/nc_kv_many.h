@@ -342,6 +342,8 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   // results: a lane holds, of its row, the elements with lane index m = 8 x + 4 h2 + 0..3 of every tile
   const float l = add_halves(f.l);
   if (!live) return;
+  const int64_t places = (int64_t)a.batch * a.cache.heads * a.chunks * rows_all;
+  const int64_t place = a.chunks == 1 ? -1 : ((int64_t)bh * a.chunks + chunk) * rows_all + r;
 #pragma unroll
   for (int sg = 0; sg < L::NSEG; ++sg) {
     const int t = L::dim0(sg) / 32, dl = L::lane(sg);
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
     for (int x = 0; x < 4; ++x) {
       if (dl == 2) {
         const f32x4_t o = {f.o[t][4 * x], f.o[t][4 * x + 1], f.o[t][4 * x + 2], f.o[t][4 * x + 3]};
-        kv_store<DT>(a, sp, b, h, chunk, r, rows_all, D, L::dim0(sg) + 2 * (4 * x + 2 * h2), o, f.m, l);
+        kv_store<DT>(a, sp, h, r, D, L::dim0(sg) + 2 * (4 * x + 2 * h2), o, f.m, l, place, places);
       } else {
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc)
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
           for (int pp = 0; pp < dl / 4; ++pp) {
             const f32x4_t o = {f.o[t + 2 * pp][4 * x + 2 * cc], f.o[t + 2 * pp][4 * x + 2 * cc + 1],
                                f.o[t + 2 * pp + 1][4 * x + 2 * cc], f.o[t + 2 * pp + 1][4 * x + 2 * cc + 1]};
-            kv_store<DT>(a, sp, b, h, chunk, r, rows_all, D, L::dim0(sg) + dl * (4 * x + 2 * h2 + cc) + 4 * pp, o, f.m, l);
+            kv_store<DT>(a, sp, h, r, D, L::dim0(sg) + dl * (4 * x + 2 * h2 + cc) + 4 * pp, o, f.m, l, place, places);
           }
       }
     }
