@@ -125,6 +125,20 @@ constexpr int kKvManyRows = 128;   // rows of a workgroup of the many-row kernel
 // Most rows of a workgroup of the few-row kernel: 32 where their queries and sums fit the registers.
 constexpr int kv_few_rows(int dtype, int dim) { return dtype == NC_BF16 || dim <= 128 ? 32 : 16; }
 
+// Waves of a SIMD that the few-row kernel is compiled for: queries and sums of
+// nt row tiles, and about 110 registers more.
+constexpr int kv_few_waves(int dtype, int dim, int nt) {
+  const int need = (dtype == NC_BF16 ? 1 : 3) * nt * dim / 8 + nt * dim / 4 + 110;
+  return need <= 168 ? 3 : need <= 256 ? 2 : 1;
+}
+// Workgroups of it that the card holds at once: the shares that a call is cut into.
+constexpr int kKvUnits = 256;      // compute units
+constexpr int kv_few_slots(int dtype, int dim, int rows) {
+  const int lds = kKvFewWaves * 16 * (dim + 4) * 4 + kKvFewWaves * rows * 8, fit = 160 * 1024 / lds;
+  const int waves = kv_few_waves(dtype, dim, rows / 16);
+  return kKvUnits * (waves < fit ? waves : fit);
+}
+
 // Rows (query i of the sequence, head j of the group) are numbered i * group + j.
 // Partial results: places of D unnormalised sums, then a maximum and a sum for
 // each place.  Many rows: place ((b * heads + h) * chunks + c) * rows_all + r;

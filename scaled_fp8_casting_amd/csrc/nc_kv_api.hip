@@ -64,8 +64,8 @@ KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_
     p.most = (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / base, span / 16));
     p.chunk = (int32_t)std::max<int64_t>(1, (span + p.most - 1) / p.most);
     p.chunks = (int32_t)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
-  } else if (span > 64) {
-    p.shares = (int32_t)std::min<int64_t>(768, (base * span + kKvShareLeast - 1) / kKvShareLeast);
+  } else if (span > 128) {
+    p.shares = (int32_t)std::min<int64_t>(kv_few_slots(dtype, dim, p.rows), (base * span + kKvShareLeast - 1) / kKvShareLeast);
   }
   return p;
 }

@@ -454,41 +454,36 @@ __device__ __forceinline__ uint32_t scan64(uint32_t x, int lane) {   // inclusiv
   }
   return x;
 }
-// Tiles of all segments; with 64 sequences at most `mine` is lane i's sequence's share of them.
+// Tiles of all segments.
 __device__ __forceinline__ uint32_t kv_line(const KvAttn& a, int lane) {
   uint32_t sum = 0;
   for (int b = lane; b < a.batch; b += 64) sum += (uint32_t)kv_reach(a, b).tiles;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  return sum * (uint32_t)(a.cache.heads * a.row_groups);
+  return __builtin_amdgcn_readfirstlane(sum) * (uint32_t)(a.cache.heads * a.row_groups);
 }
-// The sequence that holds tile x of the line, and where it begins.
-__device__ __forceinline__ int kv_find(const KvAttn& a, uint32_t x, int lane, uint32_t& start) {
+// The sequence that holds tile x of the line, and where on the line it begins.
+__device__ __forceinline__ int kv_find(const KvAttn& a, uint32_t x, int lane, uint32_t& start, KvReach& at) {
   const uint32_t per = (uint32_t)(a.cache.heads * a.row_groups);
   uint32_t before = 0;
   for (int b = 0; b < a.batch; b += 64) {
-    const uint32_t n = b + lane < a.batch ? (uint32_t)kv_reach(a, b + lane).tiles * per : 0u;
-    const uint32_t to = before + scan64(n, lane);
+    KvReach r = kv_reach(a, min(b + lane, a.batch - 1));
+    const uint32_t n = b + lane < a.batch ? (uint32_t)r.tiles * per : 0u, to = before + scan64(n, lane);
     const uint64_t past = __ballot(to > x);
     if (past) {
       const int i = __builtin_ctzll(past);
-      start = __builtin_amdgcn_readlane(to - n, i);
+      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, i); };
+      start = of(to - n);
+      at = KvReach{{of(r.sp.n), of(r.sp.q_len), of(r.sp.q0)}, of(r.t0), of(r.tiles)};
       return b + i;
     }
     before = __builtin_amdgcn_readlane(to, 63);
   }
-  start = before;
-  return a.batch;
+  return a.batch;                                // not reached: x is inside the line
 }
 __device__ __forceinline__ uint32_t kv_share(const KvAttn& a, uint32_t line) {
   const uint32_t n = (line + (uint32_t)a.shares - 1) / (uint32_t)a.shares;
   return max((n + 7) & ~7u, (uint32_t)kKvShareLeast);
-}
-
-// Waves of a SIMD to compile for.
-constexpr int few_waves_simd(int dtype, int dim, int nt) {
-  const int need = (dtype == NC_BF16 ? 1 : 3) * nt * dim / 8 + nt * dim / 4 + 110;
-  return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
 }
 
 // One segment's tiles [t0, t1): the workgroup's sums into the result (place < 0)
@@ -557,7 +552,8 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
     if (kb <= ka || __ballot(mine && ids < 0)) ka = kb = 0;
     KvRegs<FMT, D> r[KT];
     auto tile = [&](int k, int j) {
-      return a.cache.data + (int64_t)max(__builtin_amdgcn_readlane(ids, (k * KT + j) & 63), 0) * L::TILE;
+      // a tile that is missing: some tile of the cache, masked
+      return a.cache.data + (int64_t)max(__builtin_amdgcn_readlane(ids, k * KT + j), 0) * L::TILE;
     };
     auto keys = [&](int k) {
 #pragma unroll
@@ -640,7 +636,7 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
 
 
 template <int FMT, int D, int DT, int NT, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, few_waves_simd(DT, D, NT)) kv_few(KvAttn a) {
+__global__ void __launch_bounds__(64 * WAVES, kv_few_waves(DT, D, NT)) kv_few(KvAttn a) {
   // one row tile's sums of every wave, then every row's maximum and sum
   __shared__ __align__(16) float lds[WAVES * 16 * (D + 4) + WAVES * 16 * NT * 2];
   const uint32_t per = (uint32_t)(a.cache.heads * a.row_groups);
@@ -656,12 +652,11 @@ __global__ void __launch_bounds__(64 * WAVES, few_waves_simd(DT, D, NT)) kv_few(
     if (to == 0) return;
   } else {
     const int lane = threadIdx.x & 63;
-    const uint32_t line = __builtin_amdgcn_readfirstlane(kv_line(a, lane)), share = kv_share(a, line);
+    const uint32_t line = kv_line(a, lane), share = kv_share(a, line);
     x = blockIdx.x * share;
     to = min(line, x + share);
     if (x >= to) return;
-    b = __builtin_amdgcn_readfirstlane(kv_find(a, x, lane, start));
-    r = kv_reach_wave(a, b);
+    b = kv_find(a, x, lane, start, r);
     seg = (x - start) / (uint32_t)r.tiles;
     start += seg * (uint32_t)r.tiles;
   }
@@ -690,6 +685,8 @@ hipError_t few_launch(const KvAttn& a, hipStream_t stream) {
 
 template <int FMT, int D, int DT>
 hipError_t few_by_rows(const KvAttn& a, const KvPlan& p, hipStream_t stream) {
+  if constexpr (kv_few_waves(DT, D, 1) >= 2)
+    if (p.rows == 16 && p.shares == 0) return few_launch<FMT, D, DT, 1, 2 * kKvFewWaves>(a, stream);
   if (p.rows == 16) return few_launch<FMT, D, DT, 1, kKvFewWaves>(a, stream);
   if constexpr (kv_few_rows(DT, D) == 32)
     if (p.rows == 32) return few_launch<FMT, D, DT, 2, kKvFewWaves>(a, stream);

@@ -6,7 +6,7 @@
 namespace nc {
 namespace {
 
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 
 // Places first, first + 1 * step, ... of a row, n of them; `head` is the first
 // place (it may lie off the run).
