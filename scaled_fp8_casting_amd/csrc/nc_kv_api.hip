@@ -41,7 +41,7 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
   if (s != NC_OK) return s;
   if (dtype != NC_F32 && dtype != NC_BF16) return NC_E_UNSUPPORTED;
   // one lane per eight elements, numbered in 32 bits
-  if (tokens < 0 || tokens > ((int64_t)1 << 31) || (tokens + 4) * c->heads > ((int64_t)1 << 32) / (c->dim / 8) - 256)
+  if (tokens < 0 || tokens > ((int64_t)1 << 31) || (tokens + 16) * c->heads > ((int64_t)1 << 32) / (c->dim / 8) - 256)
     return NC_E_ARG;
   if (tokens == 0) return NC_OK;
   if (k == nullptr || v == nullptr || slots == nullptr) return NC_E_ARG;

@@ -3,10 +3,10 @@
 // Both move each byte once, so HBM bandwidth bounds them.  A lane takes eight
 // elements of one row (16 bytes of bf16) -- a quarter of a block, so the
 // block's largest magnitude is two lane exchanges away -- of the key and of
-// the value.  Lanes run over the chunks of a row, then over four consecutive
-// tokens, then heads: a wave's key and value stores are then whole runs of
-// the layout (a value's dword of one token sits between those of its three
-// neighbours) when the tokens' slots follow each other, as in a prompt.
+// the value.  Lanes run over the chunks of a row, then over sixteen consecutive
+// tokens, then heads: when the tokens' slots follow each other, as in a prompt,
+// a workgroup (256 lanes) moves whole tiles and no cache line of the cache is
+// shared by workgroups on two XCDs.
 #include "nc_kv.h"
 
 namespace nc {
@@ -172,9 +172,9 @@ __device__ __forceinline__ bool item(int64_t tokens, int heads, int64_t& token, 
   const uint32_t i = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
   const uint32_t row = i / (D / 8);
   chunk = (int)(i % (D / 8));
-  const uint32_t r4 = row >> 2, quad = r4 / (uint32_t)heads;
-  head = (int)(r4 - quad * (uint32_t)heads);
-  token = (int64_t)quad * 4 + (row & 3);
+  const uint32_t t = row / kKvTokens, run = t / (uint32_t)heads;
+  head = (int)(t - run * (uint32_t)heads);
+  token = (int64_t)run * kKvTokens + row % kKvTokens;
   return token < tokens;
 }
 
@@ -264,7 +264,7 @@ NC_STREAM_KERNEL kv_read(KvCache c, KvRows<void*> k, KvRows<void*> v, const int6
 }
 
 int64_t grid_of(int64_t tokens, int heads, int dim) {
-  return ((tokens + 3) / 4 * 4 * heads * (dim / 8) + kThreads - 1) / kThreads;
+  return ((tokens + kKvTokens - 1) / kKvTokens * kKvTokens * heads * (dim / 8) + kThreads - 1) / kThreads;
 }
 
 // fn(FMT, D, DT) as compile-time values
