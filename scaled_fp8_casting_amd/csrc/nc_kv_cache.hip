@@ -212,6 +212,10 @@ NC_STREAM_KERNEL kv_write(KvCache c, KvRows<const void*> k, KvRows<const void*> 
   }
 }
 
+// The rows read are four times the codes: stored past the caches they leave them
+// to the codes (131072 tokens of 8 heads of 128, E2M1 to bf16: 94 us against 142).
+__device__ __forceinline__ void stream16(void* p, u32x4 v) { __builtin_nontemporal_store(v, static_cast<u32x4*>(p)); }
+
 template <int FMT, int DT>
 __device__ __forceinline__ void store8(void* p, int64_t at, u32x2 c, uint32_t sb) {
   const float s = kv_scale(sb);
@@ -220,7 +224,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, u32x2 c, uint32_t sb
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       r[i] = FMT == NC_E2M1 ? kv_pair<FMT>(c.x, s, i) : kv_pair<FMT>(i < 2 ? c.x : c.y, s, i & 1);
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at) = r;
+    stream16(static_cast<uint16_t*>(p) + at, r);
   } else {
     // a code's bf16 value at scale 2^0 (exact), times 2^X (exact in fp32, or rounded once in its
     // subnormal range); byte 255 is NaN
@@ -238,8 +242,8 @@ __device__ __forceinline__ void store8(void* p, int64_t at, u32x2 c, uint32_t sb
     u32x4* q = reinterpret_cast<u32x4*>(static_cast<float*>(p) + at);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      q[h] = u32x4{__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]), __float_as_uint(y[4 * h + 2]),
-                   __float_as_uint(y[4 * h + 3])};
+      stream16(q + h, u32x4{__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]), __float_as_uint(y[4 * h + 2]),
+                            __float_as_uint(y[4 * h + 3])});
   }
 }
 
