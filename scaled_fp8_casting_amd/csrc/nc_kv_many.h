@@ -9,8 +9,10 @@
 //   keys:   [8 elements u = 0..D/8-1][key 0..63][16 bytes]
 //   values: [16-key step][half h][element tile of 32][lane][quads h, 2 + h: 16 bytes]
 //
-// both read without bank conflicts by 32x32x16 bf16 products S^T = K Q^T and
-// O^T = V^T P^T.  As in the few-row kernel the scores of a query lie in one
+// each read with 16 bytes a lane by 32x32x16 bf16 products S^T = K Q^T and
+// O^T = V^T P^T.  The two halves of a wave read runs that lie 128 bytes apart
+// modulo the 256 of all banks: without that shift they met in the same banks,
+// a third of the kernel's cycles.  As in the few-row kernel the scores of a query lie in one
 // lane (and its partner 32 lanes on) in the order the second product wants
 // them.  Two LDS buffers: a step's conversion goes beside the products of the
 // step before, with one barrier between steps.
@@ -29,8 +31,8 @@ __device__ __forceinline__ f32x16_t mfma32(const u32x4& a, const u32x4& b, const
 constexpr int kManyWaves = 4, kManyKeys = 64;
 
 template <int FMT, int D> struct ManyLds {
-  uint32_t k[D / 8][kManyKeys][4];
-  uint32_t v[kManyKeys / 16][2][D / 32][32][4];
+  uint32_t k[D / 8][kManyKeys + 8][4];
+  uint32_t v[kManyKeys / 16][2][D + 8][4];
   uint32_t bad[kManyWaves];        // the wave's values hold one that is not finite (steps with masks only)
 };
 
@@ -83,7 +85,7 @@ __device__ __forceinline__ void stage(ManyLds<FMT, D>& s, const KvRegs<FMT, D>& 
           nf |= not_finite16(x.x) | not_finite16(x.y);
         }
         // quad g: half g % 2, first or second eight bytes of its operand
-        *reinterpret_cast<u32x2*>(&s.v[wave][g & 1][L::dim0(sg) / 32 + pr][2 * m + h][2 * (g >> 1)]) = x;
+        *reinterpret_cast<u32x2*>(&s.v[wave][g & 1][L::dim0(sg) + 32 * pr + 16 * h + m][2 * (g >> 1)]) = x;
       }
     }
   }
@@ -174,7 +176,7 @@ template <int FMT, int D, int DT> struct Many {
     for (int ks = 0; ks < 2 * KS; ++ks)
 #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
-        u32x4 v = *reinterpret_cast<const u32x4*>(lds.v[ks][h][t][n]);
+        u32x4 v = *reinterpret_cast<const u32x4*>(lds.v[ks][h][32 * t + n]);
         if constexpr (MASKED) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] &= ~whole16(not_finite16(v[i]));
@@ -200,7 +202,7 @@ template <int FMT, int D, int DT> struct Many {
         vis[i] = ((mine >> (2 * i)) & 1 ? 0x3F80u : 0u) | ((mine >> (2 * i)) & 2 ? 0x3F800000u : 0u);
 #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(lds.v[ks][h][t][n]);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(lds.v[ks][h][32 * t + n]);
         const u32x4 nf = {not_finite16(v[0]), not_finite16(v[1]), not_finite16(v[2]), not_finite16(v[3])};
         f32x16_t hit = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
         hit = mfma32(nf, vis, hit);
@@ -339,7 +341,8 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
     for (; k < steps; ++k) masked(k);
   }
 
-  // results: a lane holds, of its row, the elements with lane index m = 8 x + 4 h2 + 0..3 of every tile
+  // Results: of its row a lane holds, of every tile t of 32 elements, those with x = 8 e + 4 h2 + 0..3:
+  // value lane x % 16, first or second of pair t as x / 16.
   const float l = add_halves(f.l);
   if (!live) return;
   const int64_t places = (int64_t)a.batch * a.cache.heads * a.chunks * rows_all;
@@ -348,19 +351,19 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   for (int sg = 0; sg < L::NSEG; ++sg) {
     const int t = L::dim0(sg) / 32, dl = L::lane(sg);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (dl == 2) {
-        const f32x4_t o = {f.o[t][4 * x], f.o[t][4 * x + 1], f.o[t][4 * x + 2], f.o[t][4 * x + 3]};
-        kv_store<DT>(a, sp, h, r, D, L::dim0(sg) + 2 * (4 * x + 2 * h2), o, f.m, l, place, places);
+    for (int e = 0; e < 8; ++e) {
+      const int c = 8 * (e / 4) + 4 * h2 + e % 4;
+      if (dl == 2) {                             // two lanes make four elements
+        if (e % 2 == 0) {
+          const f32x4_t o = {f.o[t][e], f.o[t][e + 8], f.o[t][e + 1], f.o[t][e + 9]};
+          kv_store<DT>(a, sp, h, r, D, L::dim0(sg) + 2 * c, o, f.m, l, place, places);
+        }
       } else {
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-          for (int pp = 0; pp < dl / 4; ++pp) {
-            const f32x4_t o = {f.o[t + 2 * pp][4 * x + 2 * cc], f.o[t + 2 * pp][4 * x + 2 * cc + 1],
-                               f.o[t + 2 * pp + 1][4 * x + 2 * cc], f.o[t + 2 * pp + 1][4 * x + 2 * cc + 1]};
-            kv_store<DT>(a, sp, h, r, D, L::dim0(sg) + dl * (4 * x + 2 * h2 + cc) + 4 * pp, o, f.m, l, place, places);
-          }
+        for (int pp = 0; pp < dl / 4; ++pp) {
+          const f32x4_t o = {f.o[t + 2 * pp][e], f.o[t + 2 * pp][e + 8], f.o[t + 2 * pp + 1][e], f.o[t + 2 * pp + 1][e + 8]};
+          kv_store<DT>(a, sp, h, r, D, L::dim0(sg) + dl * c + 4 * pp, o, f.m, l, place, places);
+        }
       }
     }
   }
