@@ -101,22 +101,18 @@ struct KvAttn {
   int32_t group;           // query heads of a cache head
   int32_t causal, window;  // window 0: none
   float scale2;            // score scale times log2(e)
-  // the split: workgroups take row groups of one sequence and cache head.  Few rows:
-  // `shares` workgroups with equal shares of all tiles (0: one for each row group);
-  // many rows: `chunks` workgroups of `chunk` tiles
-  int32_t row_groups, shares, chunk, chunks;
-  float* part;             // partial results
+  // the split: row groups of one sequence and cache head, a workgroup for each or, in the few-row
+  // kernel with shares > 0, so many workgroups with equal shares of all tiles
+  int32_t row_groups, shares;
+  float* part;             // partial results of the shares
 };
 
 // What the split of a call is, from its sizes (host): shared by the workspace
 // size and the launch.
 struct KvPlan {
-  int32_t rows;         // rows of a workgroup: 16 or 32 (few), kKvManyRows
-  int32_t row_groups;   // workgroups along the rows of one (sequence, head)
-  int32_t shares;       // few: equal shares of the tiles, 0 for a workgroup to a row group
-  int32_t chunk;        // many: tiles of 16 keys of a workgroup
-  int32_t chunks;       // many: workgroups along the keys, at most `most`
-  int32_t most;         // does not fall as the span of keys grows
+  int32_t rows;         // rows of a workgroup: 16 or 32 (few-row kernel), kKvManyRows
+  int32_t row_groups;   // row groups of one (sequence, head)
+  int32_t shares;       // few rows: equal shares of the tiles, 0 for a workgroup to a row group
 };
 
 constexpr int kKvFewWaves = 4;
@@ -140,10 +136,9 @@ constexpr int kv_few_slots(int dtype, int dim, int rows) {
 }
 
 // Rows (query i of the sequence, head j of the group) are numbered i * group + j.
-// Partial results: places of D unnormalised sums, then a maximum and a sum for
-// each place.  Many rows: place ((b * heads + h) * chunks + c) * rows_all + r;
-// few rows: two for each share and row of a group.
-inline size_t kv_part_bytes(int64_t places, int dim) { return (size_t)places * (size_t)(dim + 2) * 4; }
+// Partial results: two places for each share and row of a group, of D
+// unnormalised sums, then a maximum and a sum for each place.
+inline size_t kv_part_bytes(const KvPlan& p, int dim) { return (size_t)(2 * (int64_t)p.shares * p.rows) * (size_t)(dim + 2) * 4; }
 
 hipError_t launch_kv_write(const KvCache& c, int fmt, int dim, const KvRows<const void*>& k, const KvRows<const void*>& v,
                            int dtype, const int64_t* slots, int64_t tokens, int rule, hipStream_t stream);

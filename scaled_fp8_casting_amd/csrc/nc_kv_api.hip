@@ -51,29 +51,27 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
 }
 
 // The split of a call.  span: tiles of 16 keys that a row group may reach.
+//
+// The many-row kernel does 1.6 times the work of the few-row kernel in the same
+// time once it has a workgroup for every compute unit (4096 queries over 16384
+// keys, 32 heads of 128: 0.93 ms against 1.49), and loses below that (100 over
+// 600, 5 x 32 heads, 125 workgroups: 43 us against 25; 312 workgroups: 70
+// against 67).
+//
+// Shares cost a second kernel, about 7 us; without them a workgroup runs through
+// all of its keys.  128 tiles take 8 waves 8 steps, about as long.
 KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_t rows_all, int64_t span) {
   KvPlan p = {};
-  const bool many = rows_all > 32;
-  p.rows = many ? kKvManyRows : (rows_all <= 16 ? 16 : kv_few_rows(dtype, dim));
+  if (batch * heads * ((rows_all + kKvManyRows - 1) / kKvManyRows) >= kKvUnits && rows_all > kKvManyRows / 2)
+    p.rows = kKvManyRows;
+  else
+    p.rows = rows_all <= 16 ? 16 : kv_few_rows(dtype, dim);
   p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
-  const int64_t base = std::max<int64_t>(1, batch * heads * p.row_groups);
-  p.chunks = p.most = 1;
-  p.chunk = (int32_t)std::max<int64_t>(1, span);
-  if (many) {
-    // at least 16 tiles each, at most about 512 workgroups
-    p.most = (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / base, span / 16));
-    p.chunk = (int32_t)std::max<int64_t>(1, (span + p.most - 1) / p.most);
-    p.chunks = (int32_t)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
-  } else if (span > 128) {
-    p.shares = (int32_t)std::min<int64_t>(kv_few_slots(dtype, dim, p.rows), (base * span + kKvShareLeast - 1) / kKvShareLeast);
+  if (p.rows != kKvManyRows && span > 128) {
+    const int64_t all = std::max<int64_t>(1, batch * heads * p.row_groups) * span;
+    p.shares = (int32_t)std::min<int64_t>(kv_few_slots(dtype, dim, p.rows), (all + kKvShareLeast - 1) / kKvShareLeast);
   }
   return p;
-}
-
-// Partial places of a call, those of any shorter span included.
-int64_t places_of(const KvPlan& p, int64_t batch, int64_t heads, int64_t rows_all) {
-  if (p.shares > 0) return 2 * (int64_t)p.shares * p.rows;
-  return p.most > 1 ? batch * heads * p.most * rows_all : 0;
 }
 
 int64_t span_of(int64_t max_kv, int64_t max_q, int64_t window) {
@@ -123,9 +121,8 @@ size_t nc_kv_workspace_bytes(const nc_kv_cache* c, nc_dtype dtype, int32_t q_hea
   if (check_cache(c, false) != NC_OK || (dtype != NC_F32 && dtype != NC_BF16)) return 0;
   if (check_sizes(c, q_heads, batch, max_q, max_kv) != NC_OK || batch == 0 || max_q == 0) return 0;
   const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
-  // a window only shortens the span, and a shorter span never raises the most
-  const KvPlan p = plan_of(c->dim, dtype, batch, c->heads, rows, span_of(max_kv, max_q, 0) + 1);
-  return kv_part_bytes(places_of(p, batch, c->heads, rows), c->dim);
+  // a window only shortens the span, and a shorter span never makes more shares
+  return kv_part_bytes(plan_of(c->dim, dtype, batch, c->heads, rows, span_of(max_kv, max_q, 0) + 1), c->dim);
 }
 
 nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dtype, void* ws, size_t ws_bytes,
@@ -162,18 +159,13 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   k.window = a->window;
   k.scale2 = a->scale * 1.4426950408889634f;
   const int64_t rows = (int64_t)a->max_q * k.group;
-  const KvPlan p = plan_of(c->dim, dtype, a->batch, c->heads, rows, span_of(a->max_kv, a->max_q, a->window));
+  const int64_t span = span_of(a->max_kv, a->max_q, a->window);
+  const KvPlan p = plan_of(c->dim, dtype, a->batch, c->heads, rows, span);
   k.row_groups = p.row_groups;
   k.shares = p.shares;
-  k.chunk = p.chunk;
-  k.chunks = p.chunks;
   k.part = (float*)ws;
-  const int64_t span = span_of(a->max_kv, a->max_q, a->window);
-  if ((int64_t)a->batch * c->heads * p.row_groups * std::max<int64_t>(p.chunks, span + 1) > INT32_MAX) return NC_E_ARG;
-  const bool split = p.shares > 0 || p.chunks > 1;
-  if (split && (ws == nullptr || !aligned16(ws) ||
-                ws_bytes < kv_part_bytes(places_of(p, a->batch, c->heads, rows), c->dim)))
-    return NC_E_WORKSPACE;
+  if ((int64_t)a->batch * c->heads * p.row_groups * (span + 1) > INT32_MAX) return NC_E_ARG;
+  if (p.shares > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < kv_part_bytes(p, c->dim))) return NC_E_WORKSPACE;
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e;
   const bool b16 = dtype == NC_BF16;
@@ -184,7 +176,7 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
     if (c->fmt == NC_E2M1) e = b16 ? kv_few_e2m1_bf16(k, c->dim, p, st) : kv_few_e2m1_f32(k, c->dim, p, st);
     else e = b16 ? kv_few_e4m3_bf16(k, c->dim, p, st) : kv_few_e4m3_f32(k, c->dim, p, st);
   }
-  if (e == hipSuccess && split) e = launch_kv_join(k, c->dim, dtype, p, st);
+  if (e == hipSuccess && p.shares > 0) e = launch_kv_join(k, c->dim, dtype, p, st);
   return hip_status(e);
 }
 

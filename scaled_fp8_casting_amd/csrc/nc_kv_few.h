@@ -1,5 +1,5 @@
 // Attention over the paged cache for few rows: the next tokens of running
-// sequences.
+// sequences, and prompts too small to fill the card with the many-row kernel.
 //
 // Row r = (query i, head j of the group) of a sequence and a cache head; key
 // t is seen when start(i) <= t < end(i).  With s = scale log2(e) q.k, m the
@@ -502,6 +502,7 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
   const int i_lo = row0 / a.group, i_hi = (min(rows, row0 + 16 * NT) - 1) / a.group;
   // keys that some row sees, and keys that every row sees
   const int any_end = kv_end(a, sp, i_hi), all_end = kv_end(a, sp, i_lo), all_begin = kv_begin(a, any_end);
+  t0 = max(t0, kv_begin(a, all_end) / 16);
   t1 = min(t1, (any_end + 15) >> 4);
 
   // a negative scale is the negated query's

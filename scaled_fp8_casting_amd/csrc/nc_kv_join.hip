@@ -57,26 +57,9 @@ __device__ __forceinline__ void join_row(const KvAttn& a, const KvSpan& sp, int 
   kv_result<DT>(a, sp, h, r, 4 * col, o, top, sum);
 }
 
+// A row of every segment; those that lie in one share are finished already.
 template <int D, int DT>
-__global__ void __launch_bounds__(kJoinThreads) kv_join(KvAttn a) {
-  const int rows_all = a.max_q * a.group;
-  const int r = (int)(blockIdx.x % (uint32_t)rows_all);
-  const uint32_t bh = blockIdx.x / (uint32_t)rows_all;
-  const int h = bh % (uint32_t)a.cache.heads, b = bh / (uint32_t)a.cache.heads;
-  const KvSpan sp = kv_span(a, b);
-  if (r >= sp.q_len * a.group) return;
-  KvParts p;
-  p.places = (int64_t)a.batch * a.cache.heads * a.chunks * rows_all;
-  p.head = (int64_t)bh * a.chunks * rows_all + r;
-  p.step = rows_all;
-  p.first = p.head + p.step;
-  p.n = a.chunks;
-  join_row<D, DT>(a, sp, h, r, p);
-}
-
-// The few-row kernel's shares: only segments that lie in more than one.
-template <int D, int DT>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_shares(KvAttn a, int rows) {
+__global__ void __launch_bounds__(kJoinThreads) kv_join(KvAttn a, int rows) {
   const int rows_all = a.max_q * a.group, lane = threadIdx.x & 63;
   const int r = (int)(blockIdx.x % (uint32_t)rows_all);
   const uint32_t bh = blockIdx.x / (uint32_t)rows_all;
@@ -112,8 +95,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_shares(KvAttn a, int row
 template <int D, int DT>
 hipError_t join(const KvAttn& a, const KvPlan& p, hipStream_t stream) {
   const dim3 grid((uint32_t)((int64_t)a.batch * a.cache.heads * a.max_q * a.group));
-  if (p.shares > 0) kv_join_shares<D, DT><<<grid, dim3(kJoinThreads), 0, stream>>>(a, p.rows);
-  else kv_join<D, DT><<<grid, dim3(kJoinThreads), 0, stream>>>(a);
+  kv_join<D, DT><<<grid, dim3(kJoinThreads), 0, stream>>>(a, p.rows);
   return hipGetLastError();
 }
 template <int D>

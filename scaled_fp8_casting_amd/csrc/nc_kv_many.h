@@ -29,6 +29,7 @@ __device__ __forceinline__ f32x16_t mfma32(const u32x4& a, const u32x4& b, const
 }
 
 constexpr int kManyWaves = 4, kManyKeys = 64;
+static_assert(32 * kManyWaves == kKvManyRows, "32 rows a wave");
 
 template <int FMT, int D> struct ManyLds {
   uint32_t k[D / 8][kManyKeys + 8][4];
@@ -225,20 +226,18 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   const int n = lane & 31, h2 = lane >> 5;
   // workgroup -> head and sequence first (workgroups that follow each other go to different XCDs: a
   // head's rows then share one XCD's L2 when there are a multiple of 8), rows from the last ones,
-  // which see the most keys with a causal mask, chunk of keys
+  // which see the most keys with a causal mask
   uint32_t id = blockIdx.x;
   const uint32_t bh = id % (uint32_t)(a.batch * a.cache.heads);
   id /= (uint32_t)(a.batch * a.cache.heads);
-  const int rg = a.row_groups - 1 - (int)(id % (uint32_t)a.row_groups);
-  const int chunk = id / (uint32_t)a.row_groups;
+  const int rg = a.row_groups - 1 - (int)id;
   const int h = bh % a.cache.heads, b = bh / a.cache.heads;
   const KvSpan sp = kv_span(a, b);
-  const int rows_all = a.max_q * a.group, rows = sp.q_len * a.group, row0 = rg * 32 * kManyWaves;
+  const int rows = sp.q_len * a.group, row0 = rg * kKvManyRows;
   if (row0 >= rows) return;
-  const int i_lo = row0 / a.group, i_hi = (min(rows, row0 + 32 * kManyWaves) - 1) / a.group;
+  const int i_lo = row0 / a.group, i_hi = (min(rows, row0 + kKvManyRows) - 1) / a.group;
   const int any_end = kv_end(a, sp, i_hi), any_begin = kv_begin(a, kv_end(a, sp, i_lo));
-  const int t0 = any_begin / 16 + chunk * a.chunk;
-  const int t1 = min((any_end + 15) >> 4, t0 + a.chunk);
+  const int t0 = any_begin / 16, t1 = (any_end + 15) >> 4;
 
   // this wave's rows, and the keys that some of them see
   const int wrow = row0 + 32 * wave, r = wrow + n;
@@ -345,8 +344,6 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   // value lane x % 16, first or second of pair t as x / 16.
   const float l = add_halves(f.l);
   if (!live) return;
-  const int64_t places = (int64_t)a.batch * a.cache.heads * a.chunks * rows_all;
-  const int64_t place = a.chunks == 1 ? -1 : ((int64_t)bh * a.chunks + chunk) * rows_all + r;
 #pragma unroll
   for (int sg = 0; sg < L::NSEG; ++sg) {
     const int t = L::dim0(sg) / 32, dl = L::lane(sg);
@@ -356,13 +353,13 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
       if (dl == 2) {                             // two lanes make four elements
         if (e % 2 == 0) {
           const f32x4_t o = {f.o[t][e], f.o[t][e + 8], f.o[t][e + 1], f.o[t][e + 9]};
-          kv_store<DT>(a, sp, h, r, D, L::dim0(sg) + 2 * c, o, f.m, l, place, places);
+          kv_result<DT>(a, sp, h, r, L::dim0(sg) + 2 * c, o, f.m, l);
         }
       } else {
 #pragma unroll
         for (int pp = 0; pp < dl / 4; ++pp) {
           const f32x4_t o = {f.o[t + 2 * pp][e], f.o[t + 2 * pp][e + 8], f.o[t + 2 * pp + 1][e], f.o[t + 2 * pp + 1][e + 8]};
-          kv_store<DT>(a, sp, h, r, D, L::dim0(sg) + dl * c + 4 * pp, o, f.m, l, place, places);
+          kv_result<DT>(a, sp, h, r, L::dim0(sg) + dl * c + 4 * pp, o, f.m, l);
         }
       }
     }
@@ -371,7 +368,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
 
 template <int FMT, int D, int DT>
 hipError_t many_launch(const KvAttn& a, hipStream_t stream) {
-  const int64_t grid = (int64_t)a.batch * a.cache.heads * a.row_groups * a.chunks;
+  const int64_t grid = (int64_t)a.batch * a.cache.heads * a.row_groups;
   kv_many<FMT, D, DT><<<dim3((uint32_t)grid), dim3(64 * kManyWaves), 0, stream>>>(a);
   return hipGetLastError();
 }

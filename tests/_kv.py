@@ -62,8 +62,10 @@ def tolerance(dim, dtype, out, lse, spread, reach):
 
 
 def run_case(seed, fmt, dtype, dim, heads, group, lens, q_lens, page, causal=True, window=0, rule="ceil", scale=None,
-             sliced=False, max_kv=None, mutate=None):
-    """One attention call against the oracle; returns what came back."""
+             sliced=False, max_kv=None, mutate=None, pairs=None, lose=()):
+    """One attention call against the oracle; returns what came back.  pairs: so many (sequence, query head) pairs,
+    the first and last among them, are compared (all where None).  lose: (sequence, page) entries of the table that
+    are sent outside the cache, so that their tokens are not seen."""
     rng = np.random.default_rng(seed)
     table, slots, pages = paged(rng, lens, page)
     cache = nc.new_kv_cache(pages, page, heads, dim, fmt)
@@ -85,6 +87,8 @@ def run_case(seed, fmt, dtype, dim, heads, group, lens, q_lens, page, causal=Tru
     else:
         out = torch.full_like(qd, 7.0)
     lse = torch.full(q.shape[:2], 7.0, dtype=torch.float32, device="cuda")
+    for b, at in lose:
+        table[b, at] = -1 if at % 2 else pages
     starts = torch.tensor(np.concatenate([[0], np.cumsum(q_lens)]), dtype=torch.int32, device="cuda")
     nc.nc_kv_attention(cache, qd, out, starts, torch.tensor(lens, dtype=torch.int32, device="cuda"),
                        torch.from_numpy(table).cuda(), max(q_lens), max_kv or max(lens), causal=causal, window=window,
@@ -94,17 +98,26 @@ def run_case(seed, fmt, dtype, dim, heads, group, lens, q_lens, page, causal=Tru
     sc = 1 / math.sqrt(dim) if scale is None else scale
     want_o, want_l = np.zeros(q.shape), np.full(q.shape[:2], -np.inf)
     tol_o, tol_l = np.zeros(q.shape), np.zeros(q.shape[:2])
+    got_o, got_l = f64(out), f64(lse)
+    every = len(lens) * heads * group
+    picked = set(range(every)) if pairs is None else {0, every - 1, *rng.choice(every, pairs, replace=False).tolist()}
     tk = tq = 0
-    for n, n_q in zip(lens, q_lens):
+    for b, (n, n_q) in enumerate(zip(lens, q_lens)):
         mask = kv.seen(n, n_q, causal, window)
+        for s, at in lose:
+            if s == b:
+                mask[:, at * page:(at + 1) * page] = False
         for j in range(heads * group):
             h = j // group
+            if b * heads * group + j not in picked:
+                got_o[tq:tq + n_q, j], got_l[tq:tq + n_q, j], want_l[tq:tq + n_q, j] = 0, 0, 0
+                continue
             r = kv.attend(hq[tq:tq + n_q, j], hk[tk:tk + n, h], hv[tk:tk + n, h], mask, sc)
             want_o[tq:tq + n_q, j], want_l[tq:tq + n_q, j] = r[0], r[1]
             tol_o[tq:tq + n_q, j], tol_l[tq:tq + n_q, j] = tolerance(dim, dtype, *r)
         tk += n
         tq += n_q
-    return f64(out), f64(lse), want_o, want_l, tol_o, tol_l
+    return got_o, got_l, want_o, want_l, tol_o, tol_l
 
 
 def check(got_o, got_l, want_o, want_l, tol_o, tol_l):
