@@ -84,9 +84,12 @@ def parse():
 
 
 def source_hash():
+    """Of the sources that the step's kernels come from (the key/value cache's, nc_kv*, are not among them)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "scaled_fp8_casting_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
+        if f.startswith("nc_kv"):
+            continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]

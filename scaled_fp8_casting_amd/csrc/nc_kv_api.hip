@@ -60,14 +60,23 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
 //
 // Shares cost a second kernel, about 7 us; without them a workgroup runs through
 // all of its keys.  128 tiles take 8 waves 8 steps, about as long.
+//
+// Without shares and with a compute unit for each row group of 16, groups of 16
+// rows and 8 waves take less time than half as many of 32 and 4 waves (5 queries
+// of 16 sequences over 1029 keys, 4 heads of 8 query heads: 11 us against 16);
+// with more than that the waves get in each other's way (200 over 200, 5 x 15
+// heads: 24 against 14).
+constexpr int64_t kDirectTiles = 128;
 KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_t rows_all, int64_t span) {
   KvPlan p = {};
   if (batch * heads * ((rows_all + kKvManyRows - 1) / kKvManyRows) >= kKvUnits && rows_all > kKvManyRows / 2)
     p.rows = kKvManyRows;
   else
-    p.rows = rows_all <= 16 ? 16 : kv_few_rows(dtype, dim);
+    p.rows = rows_all <= 16 || (span <= kDirectTiles && batch * heads * ((rows_all + 15) / 16) <= kKvUnits)
+                 ? 16
+                 : kv_few_rows(dtype, dim);
   p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
-  if (p.rows != kKvManyRows && span > 128) {
+  if (p.rows != kKvManyRows && span > kDirectTiles) {
     const int64_t all = std::max<int64_t>(1, batch * heads * p.row_groups) * span;
     p.shares = (int32_t)std::min<int64_t>(kv_few_slots(dtype, dim, p.rows), (all + kKvShareLeast - 1) / kKvShareLeast);
   }
