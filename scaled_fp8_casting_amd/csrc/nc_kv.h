@@ -75,12 +75,33 @@ __device__ __forceinline__ uint32_t kv_pair(uint32_t codes, float scale, int i) 
   return __builtin_bit_cast(uint32_t, r);
 }
 
+// Division by a number known to the host, of n < 2^31: with 2^s the power of two
+// not below d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + mulhi(n, m)) >> s.
+// Three instructions where the compiler's division takes some thirty: single-token
+// calls, whose code is fetched anew by every call, spend their time on such things.
+struct KvDiv {
+  uint32_t d, m, s;
+  __device__ __forceinline__ uint32_t quot(uint32_t n) const { return (n + __umulhi(n, m)) >> s; }
+  __device__ __forceinline__ uint32_t quot(uint32_t n, uint32_t& rest) const {
+    const uint32_t q = quot(n);
+    rest = n - q * d;
+    return q;
+  }
+};
+inline KvDiv kv_div(uint32_t d) {
+  uint32_t s = 0;
+  while (s < 31 && ((uint32_t)1 << s) < d) ++s;
+  return KvDiv{d, (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1), s};
+}
+
 // What a cache and a view of rows are to the kernels.
 struct KvCache {
   uint8_t* data;
   int64_t slots;        // pages * page
   int32_t page;         // tokens of a page, a multiple of 16
   int32_t heads;
+  KvDiv by_tiles;       // tiles of a page
+  KvDiv by_heads;
 };
 template <typename P> struct KvRows {   // element (token, head, i) at p[token * ts + head * hs + i]
   P p;
@@ -99,11 +120,13 @@ struct KvAttn {
   const int32_t* table;    // [batch][table_w] page numbers
   int32_t table_w, batch, total_q, max_q, max_kv;
   int32_t group;           // query heads of a cache head
+  KvDiv by_group;
   int32_t causal, window;  // window 0: none
   float scale2;            // score scale times log2(e)
   // the split: row groups of one sequence and cache head, a workgroup for each or, in the few-row
   // kernel with shares > 0, so many workgroups with equal shares of all tiles
   int32_t row_groups, shares;
+  KvDiv by_row_groups, by_segments;   // row groups; segments of a sequence, heads * row groups
   float* part;             // partial results of the shares
 };
 

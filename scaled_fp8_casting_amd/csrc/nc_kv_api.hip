@@ -32,7 +32,9 @@ nc_status check_rows(const void* p, int64_t ts, int64_t hs, nc_dtype dt) {
   return aligned16(p) && ts % unit == 0 && hs % unit == 0 ? NC_OK : NC_E_ALIGN;
 }
 
-KvCache cache_of(const nc_kv_cache* c) { return KvCache{c->data, c->pages * c->page, c->page, c->heads}; }
+KvCache cache_of(const nc_kv_cache* c) { 
+  return KvCache{c->data, c->pages * c->page, c->page, c->heads, kv_div((uint32_t)(c->page / kKvTokens)), kv_div((uint32_t)c->heads)};
+}
 nc_status hip_status(hipError_t e) { return e == hipSuccess ? NC_OK : NC_E_HIP; }
 
 nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_rows* v, int64_t tokens, nc_dtype dtype,
@@ -164,6 +166,7 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   k.max_q = a->max_q;
   k.max_kv = a->max_kv;
   k.group = a->q_heads / c->heads;
+  k.by_group = kv_div((uint32_t)k.group);
   k.causal = a->causal != 0;
   k.window = a->window;
   k.scale2 = a->scale * 1.4426950408889634f;
@@ -171,6 +174,8 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   const int64_t span = span_of(a->max_kv, a->max_q, a->window);
   const KvPlan p = plan_of(c->dim, dtype, a->batch, c->heads, rows, span);
   k.row_groups = p.row_groups;
+  k.by_row_groups = kv_div((uint32_t)p.row_groups);
+  k.by_segments = kv_div((uint32_t)(c->heads * p.row_groups));
   k.shares = p.shares;
   k.part = (float*)ws;
   if ((int64_t)a->batch * c->heads * p.row_groups * (span + 1) > INT32_MAX) return NC_E_ARG;

@@ -168,12 +168,13 @@ __device__ __forceinline__ u32x2 get_value(const uint8_t* p, int w, int step) {
 // Lane -> (token, head, chunk of eight elements); false past the end.  The
 // caller's checks keep the count of lanes below 2^32.
 template <int D>
-__device__ __forceinline__ bool item(int64_t tokens, int heads, int64_t& token, int& head, int& chunk) {
+__device__ __forceinline__ bool item(const KvCache& c, int64_t tokens, int64_t& token, int& head, int& chunk) {
   const uint32_t i = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
   const uint32_t row = i / (D / 8);
   chunk = (int)(i % (D / 8));
-  const uint32_t t = row / kKvTokens, run = t / (uint32_t)heads;
-  head = (int)(t - run * (uint32_t)heads);
+  uint32_t h;
+  const uint32_t run = c.by_heads.quot(row / kKvTokens, h);
+  head = (int)h;
   token = (int64_t)run * kKvTokens + row % kKvTokens;
   return token < tokens;
 }
@@ -182,10 +183,10 @@ __device__ __forceinline__ bool item(int64_t tokens, int heads, int64_t& token, 
 template <int FMT, int D>
 __device__ __forceinline__ bool place_of(const KvCache& c, int64_t slot, int head, int64_t& base, int& tok) {
   if (slot < 0 || slot >= c.slots) return false;
-  const uint32_t page = (uint32_t)slot / (uint32_t)c.page;     // slots are below 2^31
-  const int in = (int)((uint32_t)slot - page * (uint32_t)c.page);
-  base = (((int64_t)page * c.heads + head) * (c.page / kKvTokens) + in / kKvTokens) * Kv<FMT, D>::TILE;
-  tok = in % kKvTokens;
+  uint32_t tile;
+  const uint32_t page = c.by_tiles.quot((uint32_t)slot / kKvTokens, tile);     // slots are below 2^31
+  base = (int64_t)((page * (uint32_t)c.heads + (uint32_t)head) * c.by_tiles.d + tile) * Kv<FMT, D>::TILE;
+  tok = (int)((uint32_t)slot % kKvTokens);
   return true;
 }
 
@@ -196,7 +197,7 @@ NC_STREAM_KERNEL kv_write(KvCache c, KvRows<const void*> k, KvRows<const void*> 
   int64_t token, base = 0;
   int head, chunk, tok = 0;
   // the four lanes of a block have the same token and head, so they leave together
-  if (!item<D>(tokens, c.heads, token, head, chunk)) return;
+  if (!item<D>(c, tokens, token, head, chunk)) return;
   if (!place_of<FMT, D>(c, slots[token], head, base, tok)) return;
   uint32_t xk[8], xv[8], sk, sv;
   load8<DT>(k.p, token * k.ts + head * k.hs + chunk * 8, xk);
@@ -252,7 +253,7 @@ NC_STREAM_KERNEL kv_read(KvCache c, KvRows<void*> k, KvRows<void*> v, const int6
   using L = Kv<FMT, D>;
   int64_t token, base = 0;
   int head, chunk, tok = 0;
-  if (!item<D>(tokens, c.heads, token, head, chunk)) return;
+  if (!item<D>(c, tokens, token, head, chunk)) return;
   u32x2 ck = {0u, 0u}, cv = {0u, 0u};
   uint32_t sk = 127u, sv = 127u;                 // a slot outside the cache reads as zeros
   if (place_of<FMT, D>(c, slots[token], head, base, tok)) {

@@ -121,19 +121,21 @@ __device__ __forceinline__ int kv_begin(const KvAttn& a, int end) { return a.win
 // The number of the tile (page, head, tile of the page) that holds tokens
 // [16 t, 16 t + 16) of sequence b, or -1 for a page outside the cache.
 __device__ __forceinline__ int kv_tile_at(const KvAttn& a, int b, int h, int t) {
-  const uint32_t per = (uint32_t)a.cache.page / kKvTokens;
-  const uint32_t pg = (uint32_t)t / per;
+  const uint32_t per = a.cache.by_tiles.d;
+  uint32_t in;
+  const uint32_t pg = a.cache.by_tiles.quot((uint32_t)t, in);
   if (pg >= (uint32_t)a.table_w) return -1;
   const int32_t id = a.table[(int64_t)b * a.table_w + pg];
   if (id < 0 || (int64_t)id * a.cache.page >= a.cache.slots) return -1;
-  return (int)(((uint32_t)id * (uint32_t)a.cache.heads + (uint32_t)h) * per + ((uint32_t)t - pg * per));
+  return (int)(((uint32_t)id * (uint32_t)a.cache.heads + (uint32_t)h) * per + in);
 }
 
 // Four elements of a row's result, from its sums.
 template <int DT>
 __device__ __forceinline__ void kv_result(const KvAttn& a, const KvSpan& sp, int h, int r, int c, const f32x4_t& o, float top,
                                           float sum) {
-  const int i = r / a.group, head = h * a.group + r - i * a.group;
+  uint32_t j;
+  const int i = (int)a.by_group.quot((uint32_t)r, j), head = h * a.group + (int)j;
   const int64_t row = sp.q0 + i;
   const float x = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int64_t at = row * a.out.ts + head * a.out.hs + c;
@@ -508,7 +510,7 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
   const int m = lane & 15, g = lane >> 4;
   const int rows = sp.q_len * a.group, row0 = rg * 16 * NT;
   if (row0 >= rows) return;
-  const int i_lo = row0 / a.group, i_hi = (min(rows, row0 + 16 * NT) - 1) / a.group;
+  const int i_lo = (int)a.by_group.quot((uint32_t)row0), i_hi = (int)a.by_group.quot((uint32_t)(min(rows, row0 + 16 * NT) - 1));
   // keys that some row sees, and keys that every row sees
   const int any_end = kv_end(a, sp, i_hi), all_end = kv_end(a, sp, i_lo), all_begin = kv_begin(a, any_end);
   t0 = max(t0, kv_begin(a, all_end) / 16);
@@ -522,14 +524,15 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
   for (int t = 0; t < NT; ++t) {
     const int r = row0 + 16 * t + m;
     const bool live = r < rows;
-    const int i = live ? r / a.group : 0, j = live ? r - i * a.group : 0;
+    uint32_t j;
+    const int i = (int)a.by_group.quot(live ? (uint32_t)r : 0u, j);
     f.end[t] = kv_end(a, sp, i);
     f.begin[t] = kv_begin(a, f.end[t]);
     f.m[t] = -INFINITY;
     f.l[t] = 0;
 #pragma unroll
     for (int d = 0; d < F::MT; ++d) f.o[t][d] = f32x4_t{0, 0, 0, 0};
-    const int64_t at = (int64_t)(sp.q0 + i) * a.q.ts + (int64_t)(h * a.group + j) * a.q.hs;
+    const int64_t at = (int64_t)(sp.q0 + i) * a.q.ts + (int64_t)(h * a.group + (int)j) * a.q.hs;
 #pragma unroll
     for (int sg = 0; sg < L::NSEG; ++sg)
 #pragma unroll
@@ -654,8 +657,7 @@ __global__ void __launch_bounds__(64 * WAVES, kv_few_waves(DT, D, NT)) kv_few(Kv
   int b;
   KvReach r;
   if (a.shares == 0) {                           // a workgroup for each segment
-    b = blockIdx.x / per;
-    seg = blockIdx.x - (uint32_t)b * per;
+    b = (int)a.by_segments.quot(blockIdx.x, seg);
     r = kv_reach_wave(a, b);
     x = 0;
     to = (uint32_t)r.tiles;
@@ -672,9 +674,10 @@ __global__ void __launch_bounds__(64 * WAVES, kv_few_waves(DT, D, NT)) kv_few(Kv
   }
   for (;;) {
     const uint32_t end = start + (uint32_t)r.tiles, stop = min(end, to);
-    const int rg = seg % (uint32_t)a.row_groups, h = seg / (uint32_t)a.row_groups;
+    uint32_t rg;
+    const int h = (int)a.by_row_groups.quot(seg, rg);
     const int place = x == start && stop == end ? -1 : 2 * (int)blockIdx.x + (x == start ? 1 : 0);
-    few_segment<FMT, D, DT, NT, WAVES>(a, r.sp, b, h, rg, r.t0 + (int)(x - start), r.t0 + (int)(stop - start), place, lds);
+    few_segment<FMT, D, DT, NT, WAVES>(a, r.sp, b, h, (int)rg, r.t0 + (int)(x - start), r.t0 + (int)(stop - start), place, lds);
     x = start = stop;
     if (x >= to) return;
     if (++seg == per) {

@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join(KvAttn a, int rows) {
   const int rows_all = a.max_q * a.group, lane = threadIdx.x & 63;
   const int r = (int)(blockIdx.x % (uint32_t)rows_all);
   const uint32_t bh = blockIdx.x / (uint32_t)rows_all;
-  const int h = bh % (uint32_t)a.cache.heads, b = bh / (uint32_t)a.cache.heads;
+  uint32_t head;
+  const int b = (int)a.cache.by_heads.quot(bh, head), h = (int)head;
   const KvReach reach = kv_reach(a, b);
   if (r >= reach.sp.q_len * a.group) return;
   // where the segment lies on the line

@@ -232,20 +232,22 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   // compute unit then have different lengths (8 x 448 queries over 187 .. 1500 tokens: 44 -> 39 us).
   const uint32_t all = (uint32_t)(a.batch * a.cache.heads), turn = blockIdx.x / all, bh = blockIdx.x - turn * all;
   const int rg = a.row_groups - 1 - (int)turn;
-  const int h = bh % (uint32_t)a.cache.heads, b0 = bh / (uint32_t)a.cache.heads;
+  uint32_t h;
+  const int b0 = (int)a.cache.by_heads.quot(bh, h);
   const int b = (turn * all / kKvUnits) & 1 ? a.batch - 1 - b0 : b0;
   const KvSpan sp = kv_span(a, b);
   const int rows = sp.q_len * a.group, row0 = rg * kKvManyRows;
   if (row0 >= rows) return;
-  const int i_lo = row0 / a.group, i_hi = (min(rows, row0 + kKvManyRows) - 1) / a.group;
+  const auto query = [&](int r) { return (int)a.by_group.quot((uint32_t)r); };
+  const int i_lo = query(row0), i_hi = query(min(rows, row0 + kKvManyRows) - 1);
   const int any_end = kv_end(a, sp, i_hi), any_begin = kv_begin(a, kv_end(a, sp, i_lo));
   const int t0 = any_begin / 16, t1 = (any_end + 15) >> 4;
 
   // this wave's rows, and the keys that some of them see
   const int wrow = row0 + 32 * wave, r = wrow + n;
   const bool live = r < rows;
-  const int i = live ? r / a.group : 0, j = live ? r - i * a.group : 0;
-  const int w_lo = min(wrow, rows - 1) / a.group, w_hi = (min(rows, wrow + 32) - 1) / a.group;
+  const int i = live ? query(r) : 0, j = live ? r - i * a.group : 0;
+  const int w_lo = query(min(wrow, rows - 1)), w_hi = query(min(rows, wrow + 32) - 1);
   const int w_any_end = wrow < rows ? kv_end(a, sp, w_hi) : 0, w_any_begin = kv_begin(a, kv_end(a, sp, w_lo));
 
   Many<FMT, D, DT> f;
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   // a negative scale is the negated query's
   const float scale2 = fabsf(a.scale2);
   const uint32_t flip = a.scale2 < 0 ? 0x80008000u : 0u;
-  const int64_t at = (int64_t)(sp.q0 + i) * a.q.ts + (int64_t)(h * a.group + j) * a.q.hs;
+  const int64_t at = (int64_t)(sp.q0 + i) * a.q.ts + (int64_t)((int)h * a.group + j) * a.q.hs;
 #pragma unroll
   for (int st = 0; st < D / 16; ++st) {
     load_q<DT>(f.q[st], a.q.p, at + 16 * st + 8 * h2, live);
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   int ka = steps, kb = steps;
   {
     bool miss = false;
-    for (int t = t0 + (int)threadIdx.x; t < t1; t += 64 * kManyWaves) miss = miss || kv_tile_at(a, b, h, t) < 0;
+    for (int t = t0 + (int)threadIdx.x; t < t1; t += 64 * kManyWaves) miss = miss || kv_tile_at(a, b, (int)h, t) < 0;
     const int first = max(kv_begin(a, any_end) - 16 * t0, 0), last = min(kv_end(a, sp, i_lo) - 16 * t0, 16 * tiles);
     if (!__syncthreads_or(miss) && last > first) {
       ka = (first + kManyKeys - 1) / kManyKeys;
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
   __shared__ uint32_t have[2][kManyWaves];
   auto look_up = [&](int k) {
     const int t = t0 + 4 * (k + lane) + wave;
-    ids = t < t1 ? kv_tile_at(a, b, h, t) : -1;
+    ids = t < t1 ? kv_tile_at(a, b, (int)h, t) : -1;
   };
   auto fetch = [&](int k) {                      // past the last step: the cache's first tile, unused
     const int tile = __builtin_amdgcn_readlane(ids, k & 63);
@@ -355,13 +357,13 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
       if (dl == 2) {                             // two lanes make four elements
         if (e % 2 == 0) {
           const f32x4_t o = {f.o[t][e], f.o[t][e + 8], f.o[t][e + 1], f.o[t][e + 9]};
-          kv_result<DT>(a, sp, h, r, L::dim0(sg) + 2 * c, o, f.m, l);
+          kv_result<DT>(a, sp, (int)h, r, L::dim0(sg) + 2 * c, o, f.m, l);
         }
       } else {
 #pragma unroll
         for (int pp = 0; pp < dl / 4; ++pp) {
           const f32x4_t o = {f.o[t + 2 * pp][e], f.o[t + 2 * pp][e + 8], f.o[t + 2 * pp + 1][e], f.o[t + 2 * pp + 1][e + 8]};
-          kv_result<DT>(a, sp, h, r, L::dim0(sg) + dl * c + 4 * pp, o, f.m, l);
+          kv_result<DT>(a, sp, (int)h, r, L::dim0(sg) + dl * c + 4 * pp, o, f.m, l);
         }
       }
     }
