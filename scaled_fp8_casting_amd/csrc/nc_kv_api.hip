@@ -1,6 +1,7 @@
 // The C-ABI of the key/value cache: argument checks, the split of attention
 // over workgroups, launches.  No allocation, no state.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "nc_kv.h"
@@ -169,7 +170,9 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   k.by_group = kv_div((uint32_t)k.group);
   k.causal = a->causal != 0;
   k.window = a->window;
-  k.scale2 = a->scale * 1.4426950408889634f;
+  // at least the smallest normal number, so that a masked score of -inf stays that; a scale of 0 gives
+  // equal weights all the same
+  k.scale2 = std::copysign(std::max(std::fabs(a->scale * 1.4426950408889634f), FLT_MIN), a->scale);
   const int64_t rows = (int64_t)a->max_q * k.group;
   const int64_t span = span_of(a->max_kv, a->max_q, a->window);
   const KvPlan p = plan_of(c->dim, dtype, a->batch, c->heads, rows, span);

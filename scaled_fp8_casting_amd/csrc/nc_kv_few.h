@@ -281,24 +281,28 @@ template <int FMT, int D, int DT, int NT> struct Few {
       }
   }
 
-  // MASKED: some row sees some key of the step not, or a tile is missing (bit of `there` off).
-  template <bool MASKED>
-  __device__ __forceinline__ void weights(int base, uint32_t there, float scale2, int g) {
+  // Scores of keys that a row does not see, or of a tile that is missing (bit of `there` off): -inf.
+  __device__ __forceinline__ void mask(int base, uint32_t there, int g) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = base + 16 * j + 4 * g + i;
+          s[t][j][i] = key < end[t] && key >= begin[t] && ((there >> j) & 1) ? s[t][j][i] : -INFINITY;
+        }
+  }
+
+  __device__ __forceinline__ void weights(float scale2) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < KT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (MASKED) {
-            const int key = base + 16 * j + 4 * g + i;
-            s[t][j][i] = key < end[t] && key >= begin[t] && ((there >> j) & 1) ? s[t][j][i] : -INFINITY;
-          }
-          top = fmaxf(top, s[t][j][i]);
-        }
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][j][i]);
       top = max_groups(top) * scale2;
-      if (MASKED && !(top > -INFINITY)) top = -INFINITY;       // 0 scale times no key
       if (__ballot(top > m[t] + kGrowth)) {
         const float mn = fmaxf(m[t], top), f = m[t] == -INFINITY ? 0.0f : exp2_fast(m[t] - mn);
         l[t] *= f;
@@ -314,10 +318,6 @@ template <int FMT, int D, int DT, int NT> struct Few {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           e[i] = exp2_fast(__builtin_fmaf(s[t][j][i], scale2, -ref));
-          if constexpr (MASKED) {
-            const int key = base + 16 * j + 4 * g + i;
-            e[i] = key < end[t] && key >= begin[t] && ((there >> j) & 1) ? e[i] : 0.0f;
-          }
           sum += e[i];
         }
 #pragma unroll
@@ -337,10 +337,38 @@ template <int FMT, int D, int DT, int NT> struct Few {
     }
   }
 
-  template <bool MASKED>
-  __device__ __forceinline__ void values(const KvRegs<FMT, D> (&r)[KT], int base, uint32_t there, int n_keys, int g) {
+  // Tokens past the end, or of a tile that is missing, hold anything: codes and scales cleared.
+  // Whether what is left may hold a value that is not finite (a NaN code or scale, or a scale near
+  // the top of bf16's range).
+  static __device__ __forceinline__ bool clear(KvRegs<FMT, D> (&r)[KT], int base, uint32_t there, int n_keys, int g) {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int x = 0; x < KT; ++x) {
+      const int left = (there >> x) & 1 ? n_keys - (base + 16 * x + 4 * g) : 0;      // tokens of the quad
+      const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
+#pragma unroll
+      for (int sg = 0; sg < L::NSEG; ++sg) {
+        const int n = L::w(sg) / 16;             // bytes of a token, dwords of the quad
+        r[x].vs[sg] &= keep;
+        // a scale byte of 240 or more: (byte & 0x7F) + 16 carries into bit 7 of bytes that have it
+        odd |= r[x].vs[sg] & ((r[x].vs[sg] & 0x7F7F7F7Fu) + 0x10101010u) & 0x80808080u;
+#pragma unroll
+        for (int d = 0; d < n; ++d) {
+          uint32_t& c = r[x].v[L::off(sg) / 16 + d];
+          if (n == 4) c = left > d ? c : 0u;
+          else if (n == 2) c &= left >= 2 * d + 2 ? ~0u : left == 2 * d + 1 ? 0xFFFFu : 0u;
+          else c &= keep;
+          if constexpr (FMT == NC_E4M3) odd |= ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+        }
+      }
+    }
+    return __ballot(odd != 0) != 0;
+  }
+
+  template <bool BY_ROW>
+  __device__ __forceinline__ void values_of(const KvRegs<FMT, D> (&r)[KT], int base, uint32_t there, int n_keys, int g) {
     uint32_t keep[4];                            // tokens past the end hold anything: cleared
-    if constexpr (MASKED) {
+    if constexpr (BY_ROW) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = i / 2, key = base + 16 * j + 4 * g + 2 * (i & 1);
@@ -377,7 +405,7 @@ template <int FMT, int D, int DT, int NT> struct Few {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int d = L::dim0(sg) / 16 + 2 * pr + h;
-          if constexpr (MASKED) {
+          if constexpr (BY_ROW) {
             u32x4 nf;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -411,6 +439,13 @@ template <int FMT, int D, int DT, int NT> struct Few {
         }
       }
     }
+  }
+
+  __device__ __forceinline__ void values(const KvRegs<FMT, D> (&r)[KT]) {
+    values_of<false>(r, 0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values_by_row(const KvRegs<FMT, D> (&r)[KT], int base, uint32_t there, int n_keys, int g) {
+    values_of<true>(r, base, there, n_keys, g);
   }
 };
 
@@ -545,9 +580,9 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
   }
 
   // Steps of KT tiles, the waves in turn, 64 / KT steps at a time: lane i looks up the i-th tile
-  // that the wave takes in them.  Steps without masks come first (the order does not matter to the
-  // sums), then those that some row sees in part or that lack a page.  A step's keys and values are
-  // loaded as soon as the step before has used its own.
+  // that the wave takes in them.  A step's keys and values are loaded as soon as the step before has
+  // used its own; with masks or without, the code is the same but for the masking itself (a copy of
+  // it for the last step of a sequence took 0.8 us more: it was fetched for that step alone).
   constexpr int STRIDE = KT * WAVES, BATCH = 64 / KT;
   const int w0 = t0 + wave * KT;                 // the wave's first tile
   const int steps = w0 < t1 ? (t1 - w0 + STRIDE - 1) / STRIDE : 0;
@@ -556,17 +591,15 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
     const int t = w0 + (k0 + lane / KT) * STRIDE + lane % KT;
     const bool mine = lane < n * KT && t < t1;
     const int ids = mine ? kv_tile_at(a, b, h, t) : -1;
-    // plain steps of the batch: [ka, kb)
+    // steps without masks: [ka, kb), if no page is missing
     const int at0 = 16 * (w0 + k0 * STRIDE);
-    int ka = all_begin > at0 ? (all_begin - at0 + 16 * STRIDE - 1) / (16 * STRIDE) : 0;
-    const int whole = min(all_end, 16 * t1);
-    int kb = whole >= at0 + 16 * KT ? (whole - at0 - 16 * KT) / (16 * STRIDE) + 1 : 0;
-    kb = min(kb, n);
-    if (kb <= ka || __ballot(mine && ids < 0)) ka = kb = 0;
+    const int ka = all_begin > at0 ? (all_begin - at0 + 16 * STRIDE - 1) / (16 * STRIDE) : 0;
+    const int whole = __ballot(mine && ids < 0) ? 0 : min(all_end, 16 * t1);
+    const int kb = whole >= at0 + 16 * KT ? (whole - at0 - 16 * KT) / (16 * STRIDE) + 1 : 0;
     KvRegs<FMT, D> r[KT];
     auto tile = [&](int k, int j) {
-      // a tile that is missing: some tile of the cache, masked
-      return a.cache.data + (int64_t)max(__builtin_amdgcn_readlane(ids, k * KT + j), 0) * L::TILE;
+      // a tile that is missing, or past the last step: some tile of the cache, masked or unused
+      return a.cache.data + (int64_t)max(__builtin_amdgcn_readlane(ids, (k * KT + j) & 63), 0) * L::TILE;
     };
     auto keys = [&](int k) {
 #pragma unroll
@@ -576,28 +609,29 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
 #pragma unroll
       for (int j = 0; j < KT; ++j) load_values<FMT, D>(r[j], tile(k, j), m, g);
     };
-    if (ka < kb) {
-      keys(ka);
-      vals(ka);
-      for (int k = ka; k < kb; ++k) {
-        const int next = k + 1 < kb ? k + 1 : k;
-        f.scores(r);
-        keys(next);
-        f.template weights<false>(0, 0, scale2, g);
-        f.template values<false>(r, 0, 0, 0, g);
-        vals(next);
-      }
-    }
-    for (int k = ka > 0 ? 0 : kb; k < n; k = k + 1 == ka ? kb : k + 1) {
-      uint32_t there = 0;
-#pragma unroll
-      for (int j = 0; j < KT; ++j) there |= __builtin_amdgcn_readlane(ids, k * KT + j) >= 0 ? 1u << j : 0u;
-      const int base = at0 + 16 * STRIDE * k;
+    int base = 0;
+    uint32_t there = 0;
+    for (int k = 0;; ++k) {
       keys(k);
       vals(k);
-      f.scores(r);
-      f.template weights<true>(base, there, scale2, g);
-      f.template values<true>(r, base, there, sp.n, g);
+      for (; k < n; ++k) {
+        const bool masked = k < ka || k >= kb;
+        f.scores(r);
+        keys(k + 1);
+        if (masked) {
+          base = at0 + 16 * STRIDE * k;
+          there = 0;
+#pragma unroll
+          for (int j = 0; j < KT; ++j) there |= __builtin_amdgcn_readlane(ids, k * KT + j) >= 0 ? 1u << j : 0u;
+          f.mask(base, there, g);
+        }
+        f.weights(scale2);
+        if (masked && F::clear(r, base, there, sp.n, g)) break;
+        f.values(r);
+        vals(k + 1);
+      }
+      if (k >= n) break;
+      f.values_by_row(r, base, there, sp.n, g);  // rare: a value that is not finite and not seen by every row
     }
   }
 
