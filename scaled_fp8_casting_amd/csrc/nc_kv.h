@@ -141,8 +141,13 @@ struct KvPlan {
 constexpr int kKvFewWaves = 4;
 constexpr int kKvShareLeast = 16;  // fewest tiles of a share
 constexpr int kKvManyRows = 128;   // rows of a workgroup of the many-row kernel
-// Most rows of a workgroup of the few-row kernel: 32 where their queries and sums fit the registers.
-constexpr int kv_few_rows(int dtype, int dim) { return dtype == NC_BF16 || dim <= 128 ? 32 : 16; }
+// Most rows of a workgroup of the few-row kernel: 32 where their queries and
+// sums fit the registers.  bf16 at 256 elements does not quite (16 sequences of
+// 20000 tokens, 4 heads, 32 rows, E4M3: 160 us against 125 for groups of 16; 32
+// of 2000, 8 heads, 36 rows: 144 against 85); at 192 the groups of 32 win some
+// (5 x 5 heads, 600 rows over 200 tokens, E2M1: 19 us against 30) and lose some
+// (16 of 5500, 32 rows: 44 against 34).
+constexpr int kv_few_rows(int dtype, int dim) { return dim <= (dtype == NC_BF16 ? 192 : 128) ? 32 : 16; }
 
 // Waves of a SIMD that the few-row kernel is compiled for: queries and sums of
 // nt row tiles, and about 110 registers more.
