@@ -466,8 +466,8 @@ typedef struct {
 nc_status nc_kv_attention(const nc_kv_cache *c, const nc_kv_attn *a, nc_dtype dtype, void *ws, size_t ws_bytes,
                           void *stream);
 
-/* Workspace of nc_kv_attention for these sizes, whatever the mask; it does not
- * read c->data. */
+/* Workspace of nc_kv_attention for these and smaller batch, max_q and max_kv,
+ * whatever the mask; it does not read c->data. */
 size_t nc_kv_workspace_bytes(const nc_kv_cache *c, nc_dtype dtype, int32_t q_heads, int32_t batch, int32_t max_q,
                              int32_t max_kv);
 

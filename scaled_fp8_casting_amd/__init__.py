@@ -527,8 +527,9 @@ def kv_workspace_bytes(cache: KvCache, q: torch.Tensor, batch: int, max_q: int, 
 
 
 def new_kv_workspace(cache: KvCache, q: torch.Tensor, batch: int, max_q: int, max_kv: int) -> torch.Tensor:
-    """Device workspace for nc_kv_attention at these sizes or smaller max_q and
-    window; calls that run concurrently need workspaces of their own."""
+    """Device workspace for nc_kv_attention at these or smaller batch, max_q and
+    max_kv, whatever the window; calls that run concurrently need workspaces of
+    their own."""
     return torch.empty(max(kv_workspace_bytes(cache, q, batch, max_q, max_kv), 16), dtype=torch.uint8,
                        device=cache.device)
 

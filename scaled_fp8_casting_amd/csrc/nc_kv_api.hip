@@ -70,6 +70,11 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
 // with more than that the waves get in each other's way (200 over 200, 5 x 15
 // heads: 24 against 14).
 constexpr int64_t kDirectTiles = 128;
+int32_t shares_of(int32_t dim, nc_dtype dtype, int64_t groups, int32_t rows, int64_t span) {
+  const int64_t all = std::max<int64_t>(1, groups) * span;
+  return (int32_t)std::min<int64_t>(kv_few_slots(dtype, dim, rows), (all + kKvShareLeast - 1) / kKvShareLeast);
+}
+
 KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_t rows_all, int64_t span) {
   KvPlan p = {};
   if (batch * heads * ((rows_all + kKvManyRows - 1) / kKvManyRows) >= kKvUnits && rows_all > kKvManyRows / 2)
@@ -79,10 +84,8 @@ KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_
                  ? 16
                  : kv_few_rows(dtype, dim);
   p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
-  if (p.rows != kKvManyRows && span > kDirectTiles) {
-    const int64_t all = std::max<int64_t>(1, batch * heads * p.row_groups) * span;
-    p.shares = (int32_t)std::min<int64_t>(kv_few_slots(dtype, dim, p.rows), (all + kKvShareLeast - 1) / kKvShareLeast);
-  }
+  if (p.rows != kKvManyRows && span > kDirectTiles)
+    p.shares = shares_of(dim, dtype, batch * heads * p.row_groups, p.rows, span);
   return p;
 }
 
@@ -132,9 +135,19 @@ size_t nc_kv_workspace_bytes(const nc_kv_cache* c, nc_dtype dtype, int32_t q_hea
                              int32_t max_kv) {
   if (check_cache(c, false) != NC_OK || (dtype != NC_F32 && dtype != NC_BF16)) return 0;
   if (check_sizes(c, q_heads, batch, max_q, max_kv) != NC_OK || batch == 0 || max_q == 0) return 0;
-  const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
-  // a window only shortens the span, and a shorter span never makes more shares
-  return kv_part_bytes(plan_of(c->dim, dtype, batch, c->heads, rows, span_of(max_kv, max_q, 0) + 1), c->dim);
+  const int64_t rows = (int64_t)max_q * (q_heads / c->heads), span = span_of(max_kv, max_q, 0) + 1;
+  // Enough for every plan of these and of smaller sizes, whether this plan has
+  // shares or not: a window, and anything that shrinks, makes fewer tiles.
+  if (span <= kDirectTiles) return 0;
+  size_t most = 0;
+  for (int32_t r = 16; r <= kv_few_rows(dtype, c->dim); r += 16) {
+    KvPlan p = {};
+    p.rows = r;
+    p.shares = shares_of(c->dim, dtype, (int64_t)batch * c->heads * ((rows + r - 1) / r), r, span);
+    most = std::max(most, kv_part_bytes(p, c->dim));
+    if (rows <= 16) break;
+  }
+  return most;
 }
 
 nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dtype, void* ws, size_t ws_bytes,

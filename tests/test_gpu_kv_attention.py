@@ -204,3 +204,24 @@ def test_empty_calls():
     # a table without pages: nothing to see
     nc.nc_kv_attention(cache, q, out, i32(0, 1), i32(9), torch.empty((1, 0), dtype=torch.int32, device="cuda"), 1, 9, lse=lse)
     assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_one_workspace_for_all_calls():
+    """A prompt and single tokens of fewer, shorter sequences with the workspace of the largest sizes."""
+    dim, page, heads, kv, n_q = 64, 64, 4, 9000, 600
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pages = -(-kv // page)
+    cache = nc.new_kv_cache(2 * pages, page, heads, dim, "e2m1")
+    k, v = (torch.randn(2 * pages * page, heads, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    nc.nc_kv_write(cache, k, v, torch.arange(2 * pages * page, device="cuda"))
+    table = torch.arange(2 * pages, dtype=torch.int32, device="cuda").reshape(2, pages)
+    q = torch.randn(2 * n_q, 8 * heads, dim, generator=g, device="cuda").bfloat16()
+    ws = nc.new_kv_workspace(cache, q, 2, n_q, kv)
+    for batch, each, most in ((2, n_q, kv), (1, n_q, kv), (2, 1, kv), (1, 4, kv), (1, 1, 2500), (2, 1, 40)):
+        x = q[:batch * each]
+        starts = torch.arange(0, batch * each + 1, each, dtype=torch.int32, device="cuda")
+        lens = torch.full((batch,), most, dtype=torch.int32, device="cuda")
+        a, b = torch.empty_like(x), torch.empty_like(x)
+        nc.nc_kv_attention(cache, x, a, starts, lens, table[:batch], each, most, ws=ws)
+        nc.nc_kv_attention(cache, x, b, starts, lens, table[:batch], each, most)
+        assert torch.equal(a, b) and bool(torch.isfinite(a.float()).all())

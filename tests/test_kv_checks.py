@@ -257,3 +257,18 @@ def test_seen_and_attend():
     assert np.allclose(out, 2) and np.allclose(lse, np.log(4)) and np.allclose(spread, 2) and np.allclose(reach, np.log(3))
     out, lse, _, _ = kv.attend(q, k, v, np.array([[False, False]]), 1.0)
     assert out[0, 0] == 0 and np.isneginf(lse[0])
+
+
+@pytest.mark.parametrize("dim", (64, 192, 256))
+@pytest.mark.parametrize("dtype", (0, 1))
+def test_workspace_serves_smaller_calls(lib, dtype, dim):
+    """One workspace for the largest sizes is enough whichever of them shrink, also where the largest call itself
+    does not split its keys."""
+    c = cache(pages=40000, heads=4, dim=dim)
+    grid = [(b, q, n) for b in (1, 3, 16, 32, 200) for q in (1, 3, 9, 100, 4096) for n in (0, 40, 2048, 2100, 4100, 65536)]
+    need = {at: lib.nc_kv_workspace_bytes(c, dtype, 16, *at) for at in grid}
+    for large in grid:
+        for small in grid:
+            if all(x <= y for x, y in zip(small, large)):
+                assert need[small] <= need[large], (small, large)
+    assert need[200, 4096, 40] == 0 and need[1, 1, 65536] > 0
