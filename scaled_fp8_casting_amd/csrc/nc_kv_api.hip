@@ -62,7 +62,13 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
 // against 67).
 //
 // Shares cost a second kernel, about 7 us; without them a workgroup runs through
-// all of its keys.  128 tiles take 8 waves 8 steps, about as long.
+// all of its keys.  128 tiles take 8 waves 8 steps, about as long.  Where the row
+// groups of 16 take most of the compute units, and no more than all, shares gain
+// less and 256 tiles are run through (E2M1, heads of 128: a row group each of 32
+// sequences of 4000 tokens, 8 heads, 34 us with shares, 26 without; of 16
+// sequences of 4090 20 against 23).  Two row groups and more of 16 would be one
+// and more of 32 with shares: half of the units do there (16 sequences of 4000,
+// 4 heads, 32 rows: 30 against 25).
 //
 // Without shares and with a compute unit for each row group of 16, groups of 16
 // rows and 8 waves take less time than half as many of 32 and 4 waves (5 queries
@@ -77,14 +83,15 @@ int32_t shares_of(int32_t dim, nc_dtype dtype, int64_t groups, int32_t rows, int
 
 KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_t rows_all, int64_t span) {
   KvPlan p = {};
+  const int64_t groups = batch * heads * ((rows_all + 15) / 16);
+  const bool most = groups >= (rows_all > 16 ? kKvUnits / 2 : kKvUnits * 3 / 4) && groups <= kKvUnits;
+  const bool direct = span <= (most ? 2 * kDirectTiles : kDirectTiles);
   if (batch * heads * ((rows_all + kKvManyRows - 1) / kKvManyRows) >= kKvUnits && rows_all > kKvManyRows / 2)
     p.rows = kKvManyRows;
   else
-    p.rows = rows_all <= 16 || (span <= kDirectTiles && batch * heads * ((rows_all + 15) / 16) <= kKvUnits)
-                 ? 16
-                 : kv_few_rows(dtype, dim);
+    p.rows = rows_all <= 16 || (direct && groups <= kKvUnits) ? 16 : kv_few_rows(dtype, dim);
   p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
-  if (p.rows != kKvManyRows && span > kDirectTiles)
+  if (p.rows != kKvManyRows && !direct)
     p.shares = shares_of(dim, dtype, batch * heads * p.row_groups, p.rows, span);
   return p;
 }

@@ -225,3 +225,11 @@ def test_one_workspace_for_all_calls():
         nc.nc_kv_attention(cache, x, a, starts, lens, table[:batch], each, most, ws=ws)
         nc.nc_kv_attention(cache, x, b, starts, lens, table[:batch], each, most)
         assert torch.equal(a, b) and bool(torch.isfinite(a.float()).all())
+
+
+@pytest.mark.parametrize("fmt,dtype,dim,batch,group", [("e2m1", "bf16", 128, 32, 3), ("e4m3", "bf16", 256, 16, 17),
+                                                       ("e4m3", "fp32", 64, 40, 2), ("e2m1", "fp32", 256, 33, 16)])
+def test_many_sequences(fmt, dtype, dim, batch, group):
+    """A workgroup for a sequence's whole keys, over more of them than a few sequences would leave it; ragged."""
+    lens = [4090 - 41 * i for i in range(batch)]
+    check(*run_case(11, fmt, dtype, dim, 4, group, lens, [1] * batch, 64))
