@@ -32,7 +32,7 @@
 //
 // Measured: the next token of one sequence, 262144 tokens of 8 heads of 128 in
 // E2M1 (285 MB), 49 us and 6 us for the second kernel (5.8 TB/s; a large copy
-// reaches 5.2); 64 sequences of 1024 .. 8192 tokens 70 and 7 us (331 MB), where
+// reaches 5.2); 64 sequences of 1024 .. 8192 tokens 67 and 7 us (331 MB), where
 // the waves wait at every change of sequence; 517 tokens 8 us, of which 5.6 are
 // there for 32 tokens already (dependent loads: lengths, table, codes).  Wider
 // steps (four tiles, 170 registers and more) left one wave a SIMD: 110 us.  The
