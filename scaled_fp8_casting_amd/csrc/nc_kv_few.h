@@ -116,7 +116,8 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttn& a, int b) {
 __device__ __forceinline__ int kv_end(const KvAttn& a, const KvSpan& s, int i) {
   return a.causal ? min(s.n, s.n - s.q_len + 1 + i) : s.n;
 }
-__device__ __forceinline__ int kv_begin(const KvAttn& a, int end) { return a.window ? max(0, end - a.window) : 0; }
+// max(0, end - window), without a difference that 32 bits do not hold: end may be as low as 1 - max_q.
+__device__ __forceinline__ int kv_begin(const KvAttn& a, int end) { return a.window ? max(end, a.window) - a.window : 0; }
 
 // The number of the tile (page, head, tile of the page) that holds tokens
 // [16 t, 16 t + 16) of sequence b, or -1 for a page outside the cache.
