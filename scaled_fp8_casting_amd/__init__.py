@@ -410,6 +410,7 @@ def nc_swamp_window(pol: NcSwampPolicy, st: torch.Tensor, in_counts: torch.Tenso
 # -- the key/value cache -------------------------------------------------------
 
 KV_FMT = {"e2m1": NC_E2M1, "e4m3": NC_E4M3}
+_I32_MAX = 2 ** 31 - 1
 
 
 class KvCache:
@@ -441,7 +442,8 @@ def kv_page_bytes(page: int, heads: int, dim: int, fmt: str) -> int:
         raise ValueError(f"page {page}: a positive multiple of 16")
     if heads < 1 or dim not in (64, 96, 128, 192, 256):
         raise ValueError(f"heads {heads}, dim {dim}: at least one head of 64, 96, 128, 192 or 256 elements")
-    each = int(_lib.load().nc_kv_cache_bytes(1, page, heads, dim, KV_FMT[fmt]))
+    # the library takes 32 bits of either, and ctypes would drop the rest of a longer number
+    each = 0 if max(page, heads) > _I32_MAX else int(_lib.load().nc_kv_cache_bytes(1, page, heads, dim, KV_FMT[fmt]))
     if each == 0:
         raise ValueError(f"page {page}, heads {heads}: too large")
     return each
@@ -523,6 +525,8 @@ def nc_kv_read(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor, v_out: 
 
 
 def kv_workspace_bytes(cache: KvCache, q: torch.Tensor, batch: int, max_q: int, max_kv: int) -> int:
+    if max(q.shape[1], batch, max_q, max_kv) > _I32_MAX:
+        raise ValueError(f"q_heads {q.shape[1]}, batch {batch}, max_q {max_q}, max_kv {max_kv}: at most 2^31 - 1 each")
     return int(_lib.load().nc_kv_workspace_bytes(cache.descriptor, _dtype_code(q), q.shape[1], batch, max_q, max_kv))
 
 
@@ -570,8 +574,11 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
             or not table.is_contiguous():
         raise ValueError(f"table: shape {tuple(table.shape)} of {table.dtype} on {table.device}, expected contiguous "
                          f"torch.int32 ({batch}, pages) on {dev}")
-    if max_q < 0 or max_kv < 0 or window < 0:
-        raise ValueError(f"max_q {max_q}, max_kv {max_kv}, window {window}: none may be negative")
+    window = min(window, _I32_MAX)               # more than any sequence has tokens
+    # the call's 32-bit sizes, of which ctypes would keep the low bits: none negative or above 2^31 - 1
+    if (max_q | max_kv | window | rows | q_heads | batch | table.shape[1]) >> 31:
+        raise ValueError(f"max_q {max_q}, max_kv {max_kv}, window {window}, {rows} rows, {q_heads} heads, batch {batch}, "
+                         f"{table.shape[1]} pages: none may be negative or above 2^31 - 1")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.dim)
     elif not math.isfinite(scale):

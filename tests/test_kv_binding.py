@@ -1,0 +1,106 @@
+"""What the key/value cache's binding passes to the library: sizes beyond 32 bits.
+The library is a stand-in and the tensors only say that they are on a GPU, so
+these run without one."""
+
+import pytest
+import torch
+
+import scaled_fp8_casting_amd as nc
+from scaled_fp8_casting_amd import _lib
+
+
+class OnGpu(torch.Tensor):
+    """Host memory that gives a GPU as its device."""
+    device = property(lambda self: torch.device("cuda", 0))
+
+
+def on_gpu(t):
+    return t.as_subclass(OnGpu)
+
+
+class Library:
+    """Notes the calls' arguments; sizes are the real library's."""
+
+    def __init__(self):
+        self.calls, self.real = [], _lib.load()
+
+    def nc_kv_cache_bytes(self, *args):
+        return self.real.nc_kv_cache_bytes(*args)
+
+    def nc_kv_workspace_bytes(self, *args):
+        self.calls.append(("workspace", args))
+        return 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+    monkeypatch.setattr(nc, "_kv_stream", lambda stream, dev: 0)
+    return lib
+
+
+def new_cache(heads=2, dim=64, pages=4):
+    return nc.KvCache(on_gpu(torch.zeros((pages, nc.kv_page_bytes(16, heads, dim, "e2m1")), dtype=torch.uint8)), 16, heads,
+                      dim, "e2m1")
+
+
+def rows(*shape):
+    return on_gpu(torch.zeros(shape, dtype=torch.bfloat16))
+
+
+def i32(*x):
+    return on_gpu(torch.tensor(x, dtype=torch.int32))
+
+
+def attend(cache, **kw):
+    args = dict(q=rows(3, 4, 64), out=rows(3, 4, 64), q_start=i32(0, 1, 3), kv_len=i32(9, 9),
+                table=on_gpu(torch.zeros((2, 2), dtype=torch.int32)), max_q=2, max_kv=9)
+    nc.nc_kv_attention(cache, **{**args, **kw})
+
+
+LARGE = [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63, 2 ** 70]
+
+
+@pytest.mark.parametrize("n", LARGE)
+@pytest.mark.parametrize("name", ["max_q", "max_kv"])
+def test_bounds_beyond_32_bits_are_refused(library, name, n):
+    with pytest.raises(ValueError, match=name):
+        attend(new_cache(), **{name: n})
+    assert not library.calls
+
+
+@pytest.mark.parametrize("window,passed", [(n, 2 ** 31 - 1) for n in LARGE] + [(2 ** 31 - 1, 2 ** 31 - 1), (7, 7), (0, 0)])
+def test_a_window_beyond_32_bits_is_no_limit(library, window, passed):
+    """No sequence has more than 2^31 - 1 tokens."""
+    attend(new_cache(), window=window)
+    name, args = library.calls[-1]
+    assert name == "nc_kv_attention" and args[1].window == passed
+    assert (args[1].max_q, args[1].max_kv, args[1].total_q, args[1].batch) == (2, 9, 3, 2)
+
+
+@pytest.mark.parametrize("n", LARGE)
+def test_workspace_sizes_beyond_32_bits_are_refused(library, n):
+    cache, q = new_cache(), rows(3, 4, 64)
+    for args in ((n, 1, 1), (1, n, 1), (1, 1, n)):
+        with pytest.raises(ValueError):
+            nc.kv_workspace_bytes(cache, q, *args)
+        with pytest.raises(ValueError):
+            nc.new_kv_workspace(cache, q, *args)
+    with pytest.raises(ValueError):
+        nc.kv_workspace_bytes(cache, rows(3, 1, 64).expand(3, 2 ** 32 + 2, 64), 1, 1, 1)
+    assert not library.calls
+    nc.kv_workspace_bytes(cache, q, 2 ** 31 - 1, 1, 2 ** 31 - 1)
+    assert library.calls[-1][1][2:] == (4, 2 ** 31 - 1, 1, 2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("page,heads", [(2 ** 32 + 16, 1), (2 ** 31, 1), (16, 2 ** 32 + 1), (16, 2 ** 31)])
+def test_page_sizes_beyond_32_bits_are_refused(page, heads):
+    with pytest.raises(ValueError, match="too large"):
+        nc.kv_page_bytes(page, heads, 64, "e2m1")
