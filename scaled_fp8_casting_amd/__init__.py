@@ -22,6 +22,7 @@ keeps keys and values as MX blocks of E2M1 or E4M3 codes in pages.
 import ctypes
 import math
 import struct
+from operator import attrgetter
 from typing import Optional, Sequence
 
 import torch
@@ -417,21 +418,37 @@ class KvCache:
     """Keys and values of past tokens as MX blocks, in pages.
 
     data is one uint8 tensor of `pages` rows, a page each; pages may be copied
-    as rows.  `page` tokens a page (a multiple of 16), `heads` key/value heads
-    of `dim` elements (64, 96, 128, 192 or 256), fmt "e2m1" or "e4m3"."""
+    as rows, and another tensor may take its place.  `page` tokens a page (a
+    multiple of 16), `heads` key/value heads of `dim` elements (64, 96, 128, 192
+    or 256), fmt "e2m1" or "e4m3"; these are fixed."""
 
     def __init__(self, data: torch.Tensor, page: int, heads: int, dim: int, fmt: str):
-        self.page, self.heads, self.dim, self.fmt = int(page), int(heads), int(dim), fmt
-        each = kv_page_bytes(page, heads, dim, fmt)
+        self._page, self._heads, self._dim, self._fmt = int(page), int(heads), int(dim), fmt
+        self.data = data
+
+    page, heads, dim, fmt = (property(attrgetter(name)) for name in ("_page", "_heads", "_dim", "_fmt"))
+    device, data = (property(attrgetter(name)) for name in ("_device", "_data"))
+    pages = property(lambda self: self._data.shape[0])
+
+    @data.setter
+    def data(self, data: torch.Tensor):
+        each = kv_page_bytes(self._page, self._heads, self._dim, self._fmt)
         if data.dtype != torch.uint8 or data.dim() != 2 or data.shape[1] != each or not data.is_contiguous():
             raise ValueError(f"data: shape {tuple(data.shape)} of {data.dtype}, expected contiguous "
                              f"torch.uint8 (pages, {each})")
-        self.data, self.pages, self.device = data, data.shape[0], data.device
-        if self.pages and _lib.load().nc_kv_cache_bytes(self.pages, self.page, self.heads, self.dim, KV_FMT[fmt]) == 0:
-            raise ValueError(f"{self.pages} pages: pages * page and pages * page / 16 * heads stay below 2^31")
-        # what the calls pass on; the fields above do not change afterwards
-        self.descriptor = NcKvCache(data.data_ptr() if self.pages else None, self.pages, self.page, self.heads, self.dim,
-                                    KV_FMT[fmt])
+        pages, fmt = data.shape[0], KV_FMT[self._fmt]
+        if pages and _lib.load().nc_kv_cache_bytes(pages, self._page, self._heads, self._dim, fmt) == 0:
+            raise ValueError(f"{pages} pages: pages * page and pages * page / 16 * heads stay below 2^31")
+        self._data, self._at, self._shape, self._device = data, data.data_ptr(), data.shape, data.device
+        self._descriptor = NcKvCache(self._at if pages else None, pages, self._page, self._heads, self._dim, fmt)
+
+    @property
+    def descriptor(self) -> NcKvCache:
+        """What the calls pass on.  A tensor may be resized in place, so data is looked at every time."""
+        d = self._data
+        if d.data_ptr() != self._at or d.shape != self._shape:
+            self.data = d
+        return self._descriptor
 
 
 def kv_page_bytes(page: int, heads: int, dim: int, fmt: str) -> int:
@@ -492,6 +509,7 @@ def _kv_stream(stream, dev: torch.device) -> int:
 
 def _kv_tokens(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
     """Checks of a write or read; the call's arguments from the cache to the slots."""
+    c = cache.descriptor                         # first: it looks at data anew
     dt, dev = k.dtype, cache.device
     if dt not in _KV_DTYPE:
         raise TypeError(f"dtype {dt} (float32 or bfloat16 expected)")
@@ -504,7 +522,7 @@ def _kv_tokens(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Te
     ks, vs = _rows(k, "k", shape, dt, unit, dev), _rows(v, "v", shape, dt, unit, dev)
     if dev.type != "cuda":
         raise ValueError("device tensor expected (no CPU path)")
-    return cache.descriptor, NcKvRows(*ks), NcKvRows(*vs), tokens, code, slots.data_ptr()
+    return c, NcKvRows(*ks), NcKvRows(*vs), tokens, code, slots.data_ptr()
 
 
 def nc_kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule="ceil", stream=None):
@@ -551,6 +569,7 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
     (cross attention).  window: tokens that a query sees at most, 0 for all.
     scale: 1 / sqrt(dim) where None.  lse (fp32 [rows, q_heads]) receives
     log sum exp of the scores; a query that sees nothing gets out 0, lse -inf."""
+    c = cache.descriptor                         # first: it looks at data anew
     dt, dev, shape = q.dtype, cache.device, q.shape
     if dt not in _KV_DTYPE:
         raise TypeError(f"q: dtype {dt} (float32 or bfloat16 expected)")
@@ -597,7 +616,6 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
         raise ValueError("device tensor expected (no CPU path)")
     if rows == 0 or batch == 0 or max_q == 0:
         return
-    c = cache.descriptor
     lib = _lib.load()
     if ws is None:
         need = int(lib.nc_kv_workspace_bytes(c, code, q_heads, batch, max_q, max_kv))

@@ -104,3 +104,54 @@ def test_workspace_sizes_beyond_32_bits_are_refused(library, n):
 def test_page_sizes_beyond_32_bits_are_refused(page, heads):
     with pytest.raises(ValueError, match="too large"):
         nc.kv_page_bytes(page, heads, 64, "e2m1")
+
+
+# -- a cache's memory ------------------------------------------------------------
+
+def passed(library, cache):
+    """What the calls pass on of the cache."""
+    seen = []
+    x = rows(3, 2, 64)
+    nc.nc_kv_write(cache, x, x, on_gpu(torch.arange(3)))
+    nc.nc_kv_read(cache, on_gpu(torch.arange(3)), x, rows(3, 2, 64))
+    attend(cache)
+    for name, args in library.calls:
+        seen.append((args[0].data, args[0].pages, args[0].page, args[0].heads, args[0].dim))
+    library.calls.clear()
+    assert seen
+    return set(seen)
+
+
+def test_calls_follow_assigned_memory(library):
+    cache = new_cache()
+    assert passed(library, cache) == {(cache.data.data_ptr(), 4, 16, 2, 64)}
+    old = cache.data
+    cache.data = on_gpu(torch.zeros((7, old.shape[1]), dtype=torch.uint8))
+    assert cache.pages == 7 and old.data_ptr() != cache.data.data_ptr()
+    assert passed(library, cache) == {(cache.data.data_ptr(), 7, 16, 2, 64)}
+    for bad in (on_gpu(torch.zeros((7, old.shape[1] - 1), dtype=torch.uint8)), on_gpu(torch.zeros((7, old.shape[1]))),
+                on_gpu(torch.zeros(old.shape[1], dtype=torch.uint8))):
+        with pytest.raises(ValueError, match="data: shape"):
+            cache.data = bad
+    assert passed(library, cache) == {(cache.data.data_ptr(), 7, 16, 2, 64)}
+
+
+def test_calls_follow_resized_memory(library):
+    cache = new_cache()
+    each = cache.data.shape[1]
+    for pages in (2000, 3, 0):
+        cache.data.resize_(pages, each)
+        assert passed(library, cache) == {(cache.data.data_ptr() if pages else None, pages, 16, 2, 64)}
+        assert cache.pages == pages
+    cache = new_cache()
+    cache.data.resize_(4, each - 1)
+    with pytest.raises(ValueError, match="data: shape"):
+        attend(cache)
+    assert not [c for c in library.calls if c[0] != "workspace"]
+
+
+@pytest.mark.parametrize("name", ["page", "heads", "dim", "fmt", "pages", "device", "descriptor"])
+def test_sizes_are_fixed(name):
+    cache = new_cache()
+    with pytest.raises(AttributeError):
+        setattr(cache, name, getattr(cache, name))
