@@ -507,6 +507,18 @@ def _kv_stream(stream, dev: torch.device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _kv_call(dev: torch.device, name: str, *args):
+    """The library's call with the cache's GPU as the current one: a default stream's number is 0 on every GPU,
+    and means the current one's."""
+    call = getattr(_lib.load(), name)
+    if torch._C._cuda_getDevice() == dev.index:  # torch.cuda.current_device(), for a GPU that is in use
+        status = call(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args)
+    _check(status, name)
+
+
 def _kv_tokens(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
     """Checks of a write or read; the call's arguments from the cache to the slots."""
     c = cache.descriptor                         # first: it looks at data anew
@@ -531,7 +543,7 @@ def nc_kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
     may be slices of a fused projection."""
     r = MX_RULE[rule] if isinstance(rule, str) else rule
     args = _kv_tokens(cache, k, v, slots)
-    _check(_lib.load().nc_kv_write(*args, r, _kv_stream(stream, cache.device)), "nc_kv_write")
+    _kv_call(cache.device, "nc_kv_write", *args, r, _kv_stream(stream, cache.device))
 
 
 def nc_kv_read(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
@@ -539,7 +551,7 @@ def nc_kv_read(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor, v_out: 
     _spread(k_out, "k")
     _spread(v_out, "v")
     args = _kv_tokens(cache, k_out, v_out, slots)
-    _check(_lib.load().nc_kv_read(*args, _kv_stream(stream, cache.device)), "nc_kv_read")
+    _kv_call(cache.device, "nc_kv_read", *args, _kv_stream(stream, cache.device))
 
 
 def kv_workspace_bytes(cache: KvCache, q: torch.Tensor, batch: int, max_q: int, max_kv: int) -> int:
@@ -616,9 +628,8 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
         raise ValueError("device tensor expected (no CPU path)")
     if rows == 0 or batch == 0 or max_q == 0:
         return
-    lib = _lib.load()
     if ws is None:
-        need = int(lib.nc_kv_workspace_bytes(c, code, q_heads, batch, max_q, max_kv))
+        need = int(_lib.load().nc_kv_workspace_bytes(c, code, q_heads, batch, max_q, max_kv))
         if need:
             # on the call's own stream: freed memory is handed out again in that stream's order
             on = torch.cuda.current_stream(dev) if stream is None else (
@@ -628,4 +639,4 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
     a = NcKvAttn(*qs, *os, lat, lts, q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), table.shape[1], batch, rows,
                  q_heads, max_q, max_kv, 1 if causal else 0, window, scale)
     wat, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
-    _check(lib.nc_kv_attention(c, a, code, wat, wn, _kv_stream(stream, dev)), "nc_kv_attention")
+    _kv_call(dev, "nc_kv_attention", c, a, code, wat, wn, _kv_stream(stream, dev))

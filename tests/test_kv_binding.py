@@ -27,6 +27,9 @@ class Library:
     def nc_kv_cache_bytes(self, *args):
         return self.real.nc_kv_cache_bytes(*args)
 
+    def nc_status_string(self, status):
+        return self.real.nc_status_string(status)
+
     def nc_kv_workspace_bytes(self, *args):
         self.calls.append(("workspace", args))
         return 0
@@ -43,6 +46,7 @@ def library(monkeypatch):
     lib = Library()
     monkeypatch.setattr(_lib, "load", lambda: lib)
     monkeypatch.setattr(nc, "_kv_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     return lib
 
 
@@ -155,3 +159,52 @@ def test_sizes_are_fixed(name):
     cache = new_cache()
     with pytest.raises(AttributeError):
         setattr(cache, name, getattr(cache, name))
+
+
+# -- the GPU that a call is made on -------------------------------------------------
+
+class Devices:
+    """Stands for torch.cuda's current device."""
+
+    def __init__(self, monkeypatch, now):
+        self.now = now
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.now, raising=False)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.now)
+        devices = self
+
+        class Device:
+            def __init__(self, to):
+                self.to = to.index if isinstance(to, torch.device) else to
+
+            def __enter__(self):
+                self.before, devices.now = devices.now, self.to
+
+            def __exit__(self, *exc):
+                devices.now = self.before
+
+        monkeypatch.setattr(torch.cuda, "device", Device)
+
+
+@pytest.mark.parametrize("now", [0, 1])
+def test_calls_are_made_on_the_caches_gpu(monkeypatch, library, now):
+    """A stream's number 0 means the current device's default stream, so the cache's has to be current."""
+    devices = Devices(monkeypatch, now)
+    on = []
+    monkeypatch.setattr(library, "calls", type("Calls", (list,), {"append": lambda self, call: on.append(
+        (call[0], devices.now))})())
+    cache, x = new_cache(), rows(3, 2, 64)
+    nc.nc_kv_write(cache, x, x, on_gpu(torch.arange(3)))
+    nc.nc_kv_read(cache, on_gpu(torch.arange(3)), x, rows(3, 2, 64))
+    attend(cache)
+    attend(cache, ws=on_gpu(torch.zeros(16, dtype=torch.uint8)), stream=0)
+    assert {name for name, _ in on} >= {"nc_kv_write", "nc_kv_read", "nc_kv_attention"}
+    assert all(at == 0 for name, at in on if name != "workspace"), on
+    assert devices.now == now
+
+
+def test_the_device_is_set_back_after_a_refusal(monkeypatch, library):
+    devices = Devices(monkeypatch, 1)
+    library.nc_kv_write = lambda *args: 5
+    with pytest.raises(nc.NarrowcastError):
+        nc.nc_kv_write(new_cache(), rows(3, 2, 64), rows(3, 2, 64), on_gpu(torch.arange(3)))
+    assert devices.now == 1
