@@ -434,6 +434,10 @@ nc_status nc_kv_read(const nc_kv_cache *c, const nc_kv_rows *k, const nc_kv_rows
  * queries (its rows of out are left as they were), and tokens on a page
  * outside the cache are not seen.
  *
+ * Sizes: with rows = max_q * q_heads / heads, any call with batch * heads * rows
+ * below 2^31 and batch * heads * (rows / 16, rounded up) below 2^23 is served;
+ * larger ones may get NC_E_ARG.
+ *
  * A cached NaN that a query sees makes its lse and out NaN (of a value: the
  * elements concerned).  Tokens past kv_len may hold anything. */
 typedef struct {

@@ -75,7 +75,11 @@ nc_status check_tokens(const nc_kv_cache* c, const nc_kv_rows* k, const nc_kv_ro
 // of 16 sequences over 1029 keys, 4 heads of 8 query heads: 11 us against 16);
 // with more than that the waves get in each other's way (200 over 200, 5 x 15
 // heads: 24 against 14).
+//
+// Shares number all tiles of all row groups in 31 bits, and joining them takes 256 threads for each row; a call
+// that may have more goes without them.
 constexpr int64_t kDirectTiles = 128;
+constexpr int64_t kMostThreads = UINT32_MAX;   // of a launch
 int32_t shares_of(int32_t dim, nc_dtype dtype, int64_t groups, int32_t rows, int64_t span) {
   const int64_t all = std::max<int64_t>(1, groups) * span;
   return (int32_t)std::min<int64_t>(kv_few_slots(dtype, dim, rows), (all + kKvShareLeast - 1) / kKvShareLeast);
@@ -91,8 +95,10 @@ KvPlan plan_of(int32_t dim, nc_dtype dtype, int64_t batch, int64_t heads, int64_
   else
     p.rows = rows_all <= 16 || (direct && groups <= kKvUnits) ? 16 : kv_few_rows(dtype, dim);
   p.row_groups = (int32_t)((rows_all + p.rows - 1) / p.rows);
-  if (p.rows != kKvManyRows && !direct)
-    p.shares = shares_of(dim, dtype, batch * heads * p.row_groups, p.rows, span);
+  const int64_t segments = batch * heads;
+  if (p.rows != kKvManyRows && !direct && segments * p.row_groups <= INT32_MAX / (span + 1) &&
+      segments * rows_all <= kMostThreads / 256)
+    p.shares = shares_of(dim, dtype, segments * p.row_groups, p.rows, span);
   return p;
 }
 
@@ -201,7 +207,7 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   k.by_segments = kv_div((uint32_t)(c->heads * p.row_groups));
   k.shares = p.shares;
   k.part = (float*)ws;
-  if ((int64_t)a->batch * c->heads * p.row_groups * (span + 1) > INT32_MAX) return NC_E_ARG;
+  if ((int64_t)a->batch * c->heads * p.row_groups > kMostThreads / 512) return NC_E_ARG;   // 256 or 512 threads each
   if (p.shares > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < kv_part_bytes(p, c->dim))) return NC_E_WORKSPACE;
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e;
