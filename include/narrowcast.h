@@ -428,8 +428,8 @@ nc_status nc_kv_read(const nc_kv_cache *c, const nc_kv_rows *k, const nc_kv_rows
  *   out = sum_t softmax_t(scale * q.k_t) v_t,  lse = log sum_t exp(scale * q.k_t);
  * a query that sees none gets out = 0 and lse = -inf.
  *
- * The arrays in device memory are not trusted: kv_len is cut to max_kv and to
- * what the table holds, a negative one counts as 0, more than max_q queries
+ * The arrays in device memory are not trusted: kv_len is cut to max_kv, to
+ * what the table holds and to 2^31 - 16, a negative one counts as 0, more than max_q queries
  * are cut, q_start that decreases or passes total_q gives that sequence no
  * queries (its rows of out are left as they were), and tokens on a page
  * outside the cache are not seen.

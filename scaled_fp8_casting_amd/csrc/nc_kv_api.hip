@@ -191,7 +191,7 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   k.batch = a->batch;
   k.total_q = a->total_q;
   k.max_q = a->max_q;
-  k.max_kv = a->max_kv;
+  k.max_kv = std::min(a->max_kv, INT32_MAX - 15);   // a cache's most; the end of its last tile is 2^31 - 16
   k.group = a->q_heads / c->heads;
   k.by_group = kv_div((uint32_t)k.group);
   k.causal = a->causal != 0;

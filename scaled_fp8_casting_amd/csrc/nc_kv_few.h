@@ -112,7 +112,7 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttn& a, int b) {
   s.q_len = ok ? min(q1 - q0, a.max_q) : 0;
   return s;
 }
-// Query i sees keys [kv_start, kv_end).
+// Query i sees keys [kv_begin, kv_end).
 __device__ __forceinline__ int kv_end(const KvAttn& a, const KvSpan& s, int i) {
   return a.causal ? min(s.n, s.n - s.q_len + 1 + i) : s.n;
 }
@@ -596,7 +596,7 @@ __device__ __forceinline__ void few_segment(const KvAttn& a, const KvSpan& sp, i
     const int at0 = 16 * (w0 + k0 * STRIDE);
     const int ka = all_begin > at0 ? (all_begin - at0 + 16 * STRIDE - 1) / (16 * STRIDE) : 0;
     const int whole = __ballot(mine && ids < 0) ? 0 : min(all_end, 16 * t1);
-    const int kb = whole >= at0 + 16 * KT ? (whole - at0 - 16 * KT) / (16 * STRIDE) + 1 : 0;
+    const int kb = whole - at0 >= 16 * KT ? (whole - at0 - 16 * KT) / (16 * STRIDE) + 1 : 0;
     KvRegs<FMT, D> r[KT];
     auto tile = [&](int k, int j) {
       // a tile that is missing, or past the last step: some tile of the cache, masked or unused

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves_simd(DT, D)) kv_ma
     if (k + 1 < steps) put(k + 1);
     fetch(k + 2);
     const int base = (t0 + 4 * k) * 16;
-    if (base >= w_any_end || base + kManyKeys <= w_any_begin) return;
+    if (base >= w_any_end || w_any_begin - base >= kManyKeys) return;
     uint32_t all = 0;
 #pragma unroll
     for (int w = 0; w < kManyWaves; ++w) all |= have[k & 1][w] ? 1u << w : 0u;

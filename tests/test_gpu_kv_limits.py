@@ -51,3 +51,50 @@ def test_many_sequences_of_possibly_long_prompts():
 def test_many_sequences_of_possibly_long_caches():
     """Single tokens of 4096 sequences of up to 2^20: 2.1e9 tiles."""
     served(1, 1 << 20, 4096, [3000, 77], [1, 1], 8)
+
+
+LONG = 1 << 20       # tokens of a page that stands for every page of a sequence of 2^31
+
+
+def long_cache(batch):
+    g = torch.Generator(device="cuda").manual_seed(9)
+    cache = nc.new_kv_cache(1, LONG, 1, 64, "e2m1")
+    k, v = (torch.randn(LONG, 1, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    nc.nc_kv_write(cache, k, v, torch.arange(LONG, device="cuda"))
+    return g, cache, torch.zeros((batch, 2 ** 31 // LONG), dtype=torch.int32, device="cuda")
+
+
+def last(cache, q, table, batch, n_q, n, **kw):
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    start = torch.arange(0, batch * n_q + 1, n_q, dtype=torch.int32, device="cuda")
+    nc.nc_kv_attention(cache, q, out, start, torch.full((batch,), n, dtype=torch.int32, device="cuda"), table, n_q, n, lse=lse,
+                       **kw)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("n", [2 ** 31 - 16, 2 ** 31 - 1])
+def test_the_longest_sequence(n):
+    """2^31 - 16 tokens, a cache's most: one page 2047 times and, but for its last 16 tokens, once more."""
+    g, cache, table = long_cache(1)
+    q = torch.randn(1, 2, 64, generator=g, device="cuda")
+    out, lse = last(cache, q, table, 1, 1, n)
+    (o1, l1), (o2, l2) = (last(cache, q, table[:, :1].contiguous(), 1, 1, m) for m in (LONG, LONG - 16))
+    w1, w2 = 2047 * torch.exp(l1.double()), torch.exp(l2.double())
+    want = (o1 * w1[..., None] + o2 * w2[..., None]) / (w1 + w2)[..., None]
+    # a lane sums the weights of 1 of 4 keys, of a wave of at least 4 x 256: 2^31 / 2^12 terms, each addition off by
+    # 2^-24 of the sum at most
+    off = 2.0 ** 19 * 2.0 ** -24
+    assert ((lse - torch.log(w1 + w2)).abs() <= off).all()
+    assert ((out - want).abs() <= 2 * off * 6).all()      # no value is above 6
+
+
+@pytest.mark.parametrize("n_q,batch,group", [(130, 128, 2), (3, 2, 4)])
+@pytest.mark.parametrize("window", [100, 116, 132, 148])
+def test_the_last_tokens_of_the_longest_sequences(window, n_q, batch, group):
+    """The same tokens, in the same places of their tiles and steps, as those of a sequence of one page."""
+    g, cache, table = long_cache(batch)
+    q = torch.randn(batch * n_q, group, 64, generator=g, device="cuda").bfloat16()
+    got = last(cache, q, table, batch, n_q, 2 ** 31 - 16, window=window)
+    want = last(cache, q, table[:, :1].contiguous(), batch, n_q, LONG - 16, window=window)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
