@@ -458,7 +458,8 @@ typedef struct {
   int32_t max_kv;           /* nor more cached tokens */
   int32_t causal;           /* 0/1 */
   int32_t window;           /* tokens that a query sees at most; 0: no window */
-  float scale;              /* finite; 1 / sqrt(dim) is usual */
+  float scale;              /* 1 / sqrt(dim) is usual; scale * log2(e) is finite, and counts as 2^-126 (of its
+                               sign) where it is nearer to 0 */
 } nc_kv_attn;
 
 /* bf16 calls round the softmax weights to bf16 before the product with the

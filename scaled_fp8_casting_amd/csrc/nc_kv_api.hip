@@ -170,7 +170,8 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   if (dtype != NC_F32 && dtype != NC_BF16) return NC_E_UNSUPPORTED;
   if (a == nullptr) return NC_E_ARG;
   if ((s = check_sizes(c, a->q_heads, a->batch, a->max_q, a->max_kv)) != NC_OK) return s;
-  if (a->total_q < 0 || a->table_pages < 0 || a->window < 0 || !std::isfinite(a->scale)) return NC_E_ARG;
+  const float scale2 = a->scale * 1.4426950408889634f;
+  if (a->total_q < 0 || a->table_pages < 0 || a->window < 0 || !std::isfinite(scale2)) return NC_E_ARG;
   if (a->batch == 0 || a->max_q == 0 || a->total_q == 0) return NC_OK;
   if (a->q_start == nullptr || a->kv_len == nullptr || (a->table == nullptr && a->table_pages > 0)) return NC_E_ARG;
   if ((s = check_rows(a->q, a->q_token_stride, a->q_head_stride, dtype)) != NC_OK) return s;
@@ -198,7 +199,7 @@ nc_status nc_kv_attention(const nc_kv_cache* c, const nc_kv_attn* a, nc_dtype dt
   k.window = a->window;
   // at least the smallest normal number, so that a masked score of -inf stays that; a scale of 0 gives
   // equal weights all the same
-  k.scale2 = std::copysign(std::max(std::fabs(a->scale * 1.4426950408889634f), FLT_MIN), a->scale);
+  k.scale2 = std::copysign(std::max(std::fabs(scale2), FLT_MIN), a->scale);
   const int64_t rows = (int64_t)a->max_q * k.group;
   const int64_t span = span_of(a->max_kv, a->max_q, a->window);
   const KvPlan p = plan_of(c->dim, dtype, a->batch, c->heads, rows, span);

@@ -49,3 +49,10 @@ def test_served(lib, kw, window):
 def test_launches_that_are_too_large(lib):
     assert call(lib, batch=1 << 21, max_q=1, max_kv=100) == _lib.NC_E_ARG
     assert call(lib, batch=1 << 20, max_q=16, max_kv=100) == _lib.NC_E_ARG
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.5e38])
+def test_scales_that_32_bits_do_not_hold(lib, scale):
+    """Scores are counted in powers of two: scale * log2(e) has to be finite."""
+    assert call(lib, scale=scale) == _lib.NC_E_ARG
+    assert call(lib, scale=2.3e38) == _lib.NC_E_HIP
