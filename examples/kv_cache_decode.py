@@ -55,7 +55,8 @@ def reference(q, k, v):
 
 
 def run(fmt="e2m1", prompts=(700, 64, 1, 333), encoder=(150, 31, 77, 410), tokens=20, seed=0):
-    """Returns the last step's results and what they are over the unquantised keys and values."""
+    """Returns the last step's results and what they are over the unquantised keys and values, its queries, and the
+    keys and values of the first encoder's states."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     batch, width = len(prompts), HEADS * (GROUP + 2)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
@@ -119,7 +120,8 @@ def run(fmt="e2m1", prompts=(700, 64, 1, 333), encoder=(150, 31, 77, 410), token
     nc.nc_kv_read(pages.cache, pages.slots(torch.zeros_like(at), at), back[0], back[1])
     torch.cuda.synchronize()
     return {"own": (own, want_own), "cross": (cross, want_cross), "keys": (back[0], seen[0][0]),
-            "values": (back[1], seen[0][1]), "bytes": pages.cache.data.numel()}
+            "values": (back[1], seen[0][1]), "query": tq, "encoder": (ek[:encoder[0]], ev[:encoder[0]]),
+            "bytes": pages.cache.data.numel()}
 
 
 def main():
