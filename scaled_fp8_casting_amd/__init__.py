@@ -483,8 +483,10 @@ def _rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, unit: in
                          f"{dtype} on {dev}")
     ts, hs, one = t.stride()
     at = t.data_ptr()
-    if shape[0] <= 1:
+    if shape[0] <= 1:                            # torch gives an axis of length 1 any stride
         ts = 0
+    if shape[1] == 1:
+        hs = 0
     if one != 1 or (ts | hs) & (unit - 1) or at & 15:
         raise ValueError(f"{name}: strides {t.stride()}: rows of adjacent elements that start on 16 bytes expected")
     return at, ts, hs

@@ -208,3 +208,19 @@ def test_the_device_is_set_back_after_a_refusal(monkeypatch, library):
     with pytest.raises(nc.NarrowcastError):
         nc.nc_kv_write(new_cache(), rows(3, 2, 64), rows(3, 2, 64), on_gpu(torch.arange(3)))
     assert devices.now == 1
+
+
+# -- strides ---------------------------------------------------------------------
+
+def test_a_single_head_has_no_stride(library):
+    """Rows of one head as the transpose of columns: torch gives the axis of length 1 the stride 1."""
+    cache = new_cache(heads=1)
+    x = rows(5, 64, 1).transpose(1, 2)
+    assert x.shape == (5, 1, 64) and x.stride() == (64, 1, 1)
+    slots = on_gpu(torch.arange(5))
+    nc.nc_kv_write(cache, x, x, slots)
+    nc.nc_kv_read(cache, slots, x, rows(5, 1, 64))
+    attend(cache, q=rows(3, 64, 1).transpose(1, 2), out=rows(3, 64, 1).transpose(1, 2))
+    write, read, attention = (args for name, args in library.calls if name != "workspace")
+    assert [(r.token_stride, r.head_stride) for r in (*write[1:3], *read[1:3])] == [(64, 0)] * 4
+    assert (attention[1].q_token_stride, attention[1].q_head_stride, attention[1].out_head_stride) == (64, 0, 0)
