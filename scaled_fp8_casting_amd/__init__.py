@@ -439,14 +439,15 @@ class KvCache:
         pages, fmt = data.shape[0], KV_FMT[self._fmt]
         if pages and _lib.load().nc_kv_cache_bytes(pages, self._page, self._heads, self._dim, fmt) == 0:
             raise ValueError(f"{pages} pages: pages * page and pages * page / 16 * heads stay below 2^31")
-        self._data, self._at, self._shape, self._device = data, data.data_ptr(), data.shape, data.device
+        self._data, self._at, self._bytes, self._device = data, data.data_ptr(), data.numel(), data.device
+        self._gpu = data.device.index if data.device.type == "cuda" else None
         self._descriptor = NcKvCache(self._at if pages else None, pages, self._page, self._heads, self._dim, fmt)
 
     @property
     def descriptor(self) -> NcKvCache:
         """What the calls pass on.  A tensor may be resized in place, so data is looked at every time."""
         d = self._data
-        if d.data_ptr() != self._at or d.shape != self._shape:
+        if d.data_ptr() != self._at or d.numel() != self._bytes:
             self.data = d
         return self._descriptor
 
@@ -503,38 +504,38 @@ def _spread(t: torch.Tensor, name: str):
         at += (size - 1) * stride
 
 
-def _kv_stream(stream, dev: torch.device) -> int:
+def _kv_stream(stream, gpu: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)     # torch.cuda.current_stream(dev), without its object
+        return torch._C._cuda_getCurrentRawStream(gpu)           # torch.cuda.current_stream(gpu), without its object
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _kv_call(dev: torch.device, name: str, *args):
+def _kv_call(cache: KvCache, name: str, call, *args):
     """The library's call with the cache's GPU as the current one: a default stream's number is 0 on every GPU,
     and means the current one's."""
-    call = getattr(_lib.load(), name)
-    if torch._C._cuda_getDevice() == dev.index:  # torch.cuda.current_device(), for a GPU that is in use
+    if torch._C._cuda_getDevice() == cache._gpu:  # torch.cuda.current_device(), for a GPU that is in use
         status = call(*args)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(cache.device):
             status = call(*args)
-    _check(status, name)
+    if status:
+        _check(status, name)
 
 
 def _kv_tokens(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
     """Checks of a write or read; the call's arguments from the cache to the slots."""
     c = cache.descriptor                         # first: it looks at data anew
     dt, dev = k.dtype, cache.device
-    if dt not in _KV_DTYPE:
+    code, unit = _KV_DTYPE.get(dt, (None, 0))
+    if code is None:
         raise TypeError(f"dtype {dt} (float32 or bfloat16 expected)")
-    code, unit = _KV_DTYPE[dt]
     if slots.dtype is not torch.int64 or slots.dim() != 1 or slots.device != dev or not slots.is_contiguous():
         raise ValueError(f"slots: shape {tuple(slots.shape)} of {slots.dtype} on {slots.device}, expected contiguous "
                          f"torch.int64, one entry a token, on {dev}")
-    tokens = slots.shape[0]
-    shape = (tokens, cache.heads, cache.dim)
+    tokens = slots.numel()
+    shape = (tokens, c.heads, c.dim)
     ks, vs = _rows(k, "k", shape, dt, unit, dev), _rows(v, "v", shape, dt, unit, dev)
-    if dev.type != "cuda":
+    if cache._gpu is None:
         raise ValueError("device tensor expected (no CPU path)")
     return c, NcKvRows(*ks), NcKvRows(*vs), tokens, code, slots.data_ptr()
 
@@ -545,7 +546,7 @@ def nc_kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
     may be slices of a fused projection."""
     r = MX_RULE[rule] if isinstance(rule, str) else rule
     args = _kv_tokens(cache, k, v, slots)
-    _kv_call(cache.device, "nc_kv_write", *args, r, _kv_stream(stream, cache.device))
+    _kv_call(cache, "nc_kv_write", _lib.load().nc_kv_write, *args, r, _kv_stream(stream, cache._gpu))
 
 
 def nc_kv_read(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
@@ -553,7 +554,7 @@ def nc_kv_read(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor, v_out: 
     _spread(k_out, "k")
     _spread(v_out, "v")
     args = _kv_tokens(cache, k_out, v_out, slots)
-    _kv_call(cache.device, "nc_kv_read", *args, _kv_stream(stream, cache.device))
+    _kv_call(cache, "nc_kv_read", _lib.load().nc_kv_read, *args, _kv_stream(stream, cache._gpu))
 
 
 def kv_workspace_bytes(cache: KvCache, q: torch.Tensor, batch: int, max_q: int, max_kv: int) -> int:
@@ -603,15 +604,16 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
     if q_start.dtype is not i32 or q_start.shape != (batch + 1,) or q_start.device != dev or not q_start.is_contiguous():
         raise ValueError(f"q_start: shape {tuple(q_start.shape)} of {q_start.dtype} on {q_start.device}, expected "
                          f"contiguous torch.int32 ({batch + 1},) on {dev}")
-    if table.dtype is not i32 or table.dim() != 2 or table.shape[0] != batch or table.device != dev \
-            or not table.is_contiguous():
+    pages = table.shape
+    if table.dtype is not i32 or len(pages) != 2 or pages[0] != batch or table.device != dev or not table.is_contiguous():
         raise ValueError(f"table: shape {tuple(table.shape)} of {table.dtype} on {table.device}, expected contiguous "
                          f"torch.int32 ({batch}, pages) on {dev}")
-    window = min(window, _I32_MAX)               # more than any sequence has tokens
+    if window > _I32_MAX:                        # more than any sequence has tokens
+        window = _I32_MAX
     # the call's 32-bit sizes, of which ctypes would keep the low bits: none negative or above 2^31 - 1
-    if (max_q | max_kv | window | rows | q_heads | batch | table.shape[1]) >> 31:
+    if (max_q | max_kv | window | rows | q_heads | batch | pages[1]) >> 31:
         raise ValueError(f"max_q {max_q}, max_kv {max_kv}, window {window}, {rows} rows, {q_heads} heads, batch {batch}, "
-                         f"{table.shape[1]} pages: none may be negative or above 2^31 - 1")
+                         f"{pages[1]} pages: none may be negative or above 2^31 - 1")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.dim)
     elif not math.isfinite(scale):
@@ -626,7 +628,7 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
         lat, lts = lse.data_ptr(), (lse.stride(0) if rows > 1 else 0)
     if ws is not None and (ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous()):
         raise ValueError(f"ws: dtype {ws.dtype} on {ws.device}, expected contiguous torch.uint8 on {dev}")
-    if dev.type != "cuda":
+    if cache._gpu is None:
         raise ValueError("device tensor expected (no CPU path)")
     if rows == 0 or batch == 0 or max_q == 0:
         return
@@ -638,7 +640,7 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
                 stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev))
             with torch.cuda.stream(on):
                 ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    a = NcKvAttn(*qs, *os, lat, lts, q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), table.shape[1], batch, rows,
+    a = NcKvAttn(*qs, *os, lat, lts, q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), pages[1], batch, rows,
                  q_heads, max_q, max_kv, 1 if causal else 0, window, scale)
     wat, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
-    _kv_call(dev, "nc_kv_attention", c, a, code, wat, wn, _kv_stream(stream, dev))
+    _kv_call(cache, "nc_kv_attention", _lib.load().nc_kv_attention, c, a, code, wat, wn, _kv_stream(stream, cache._gpu))
