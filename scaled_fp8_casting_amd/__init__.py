@@ -484,12 +484,10 @@ def _rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, unit: in
                          f"{dtype} on {dev}")
     ts, hs, one = t.stride()
     at = t.data_ptr()
-    if shape[0] <= 1:                            # torch gives an axis of length 1 any stride
-        ts = 0
-    if shape[1] == 1:
-        hs = 0
     if one != 1 or (ts | hs) & (unit - 1) or at & 15:
-        raise ValueError(f"{name}: strides {t.stride()}: rows of adjacent elements that start on 16 bytes expected")
+        ts, hs = ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0     # torch gives an axis of length 1 any stride
+        if one != 1 or (ts | hs) & (unit - 1) or at & 15:
+            raise ValueError(f"{name}: strides {t.stride()}: rows of adjacent elements that start on 16 bytes expected")
     return at, ts, hs
 
 
@@ -525,7 +523,7 @@ def _kv_call(cache: KvCache, name: str, call, *args):
 def _kv_tokens(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
     """Checks of a write or read; the call's arguments from the cache to the slots."""
     c = cache.descriptor                         # first: it looks at data anew
-    dt, dev = k.dtype, cache.device
+    dt, dev = k.dtype, cache._device
     code, unit = _KV_DTYPE.get(dt, (None, 0))
     if code is None:
         raise TypeError(f"dtype {dt} (float32 or bfloat16 expected)")
@@ -533,7 +531,7 @@ def _kv_tokens(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Te
         raise ValueError(f"slots: shape {tuple(slots.shape)} of {slots.dtype} on {slots.device}, expected contiguous "
                          f"torch.int64, one entry a token, on {dev}")
     tokens = slots.numel()
-    shape = (tokens, c.heads, c.dim)
+    shape = (tokens, cache._heads, cache._dim)
     ks, vs = _rows(k, "k", shape, dt, unit, dev), _rows(v, "v", shape, dt, unit, dev)
     if cache._gpu is None:
         raise ValueError("device tensor expected (no CPU path)")
@@ -585,13 +583,13 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
     scale: 1 / sqrt(dim) where None.  lse (fp32 [rows, q_heads]) receives
     log sum exp of the scores; a query that sees nothing gets out 0, lse -inf."""
     c = cache.descriptor                         # first: it looks at data anew
-    dt, dev, shape = q.dtype, cache.device, q.shape
+    dt, dev, shape = q.dtype, cache._device, q.shape
     if dt not in _KV_DTYPE:
         raise TypeError(f"q: dtype {dt} (float32 or bfloat16 expected)")
-    if len(shape) != 3 or shape[2] != cache.dim:
+    if len(shape) != 3 or shape[2] != cache._dim:
         raise ValueError(f"q: shape {tuple(shape)}, expected (rows, q_heads, {cache.dim})")
     rows, q_heads, _ = shape
-    if q_heads == 0 or q_heads % cache.heads:
+    if q_heads == 0 or q_heads % cache._heads:
         raise ValueError(f"q: {q_heads} heads, a multiple of the cache's {cache.heads} expected")
     code, unit = _KV_DTYPE[dt]
     qs, os = _rows(q, "q", shape, dt, unit, dev), _rows(out, "out", shape, dt, unit, dev)

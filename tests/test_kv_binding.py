@@ -219,7 +219,7 @@ def test_a_single_head_has_no_stride(library):
     assert x.shape == (5, 1, 64) and x.stride() == (64, 1, 1)
     slots = on_gpu(torch.arange(5))
     nc.nc_kv_write(cache, x, x, slots)
-    nc.nc_kv_read(cache, slots, x, rows(5, 1, 64))
+    nc.nc_kv_read(cache, slots, x, rows(5, 64, 1).transpose(1, 2))
     attend(cache, q=rows(3, 64, 1).transpose(1, 2), out=rows(3, 64, 1).transpose(1, 2))
     write, read, attention = (args for name, args in library.calls if name != "workspace")
     assert [(r.token_stride, r.head_stride) for r in (*write[1:3], *read[1:3])] == [(64, 0)] * 4
