@@ -411,8 +411,9 @@ nc_status nc_kv_write(const nc_kv_cache *c, const nc_kv_rows *k, const nc_kv_row
                       nc_dtype dtype, const int64_t *slots, nc_mx_rule rule, void *stream);
 
 /* Reads the rows at slots[i] back: y = decode(q) * 2^X, exact in fp32 (rounded
- * to nearest even below its normal range) and in bf16 (the same).  A slot
- * outside the cache reads as zeros. */
+ * to nearest even below its normal range, infinite above it, which only blocks
+ * whose largest value lies within a rounding of 2^128 reach) and in bf16 (the
+ * same).  A slot outside the cache reads as zeros. */
 nc_status nc_kv_read(const nc_kv_cache *c, const nc_kv_rows *k, const nc_kv_rows *v, int64_t tokens,
                      nc_dtype dtype, const int64_t *slots, void *stream);
 
@@ -464,7 +465,8 @@ typedef struct {
 
 /* bf16 calls round the softmax weights to bf16 before the product with the
  * values, fp32 calls keep them whole; scores, maxima, sums and products are
- * fp32.  Long caches are cut along the tokens over the workgroups; the
+ * fp32.  The work is split as if every sequence had max_q queries: prompts and
+ * single tokens are faster as two calls.  Long caches are cut along the tokens over the workgroups; the
  * partial sums go through ws (nc_kv_workspace_bytes() bytes, 16-byte aligned,
  * no initialisation; NULL when that is 0) and meet in a fixed order: the same
  * call gives the same bits. */

@@ -577,8 +577,9 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
 
     Sequence b has the rows q_start[b] .. q_start[b + 1] - 1 of q (int32,
     batch + 1) and kv_len[b] cached tokens (int32) on the pages table[b] (int32
-    [batch, pages]).  max_q and max_kv bound both on the host.  causal: the
-    queries are the sequence's last tokens; else each sees the whole cache
+    [batch, pages]).  max_q and max_kv bound both on the host; the work is split
+    as if every sequence had max_q queries, so prompts and single tokens are
+    faster as two calls.  causal: the queries are the sequence's last tokens; else each sees the whole cache
     (cross attention).  window: tokens that a query sees at most, 0 for all.
     scale: 1 / sqrt(dim) where None.  lse (fp32 [rows, q_heads]) receives
     log sum exp of the scores; a query that sees nothing gets out 0, lse -inf."""

@@ -76,7 +76,9 @@ __device__ __forceinline__ uint32_t kv_pair(uint32_t codes, float scale, int i) 
 }
 
 // Division by a number known to the host, of n < 2^31: with 2^s the power of two
-// not below d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + mulhi(n, m)) >> s.
+// not below d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + mulhi(n, m)) >> s
+// (T. Granlund, P. L. Montgomery, "Division by Invariant Integers using
+// Multiplication", PLDI 1994, section 4; the sum does not overflow here).
 // Three instructions where the compiler's division takes some thirty: single-token
 // calls, whose code is fetched anew by every call, spend their time on such things.
 struct KvDiv {
@@ -123,8 +125,9 @@ struct KvAttn {
   KvDiv by_group;
   int32_t causal, window;  // window 0: none
   float scale2;            // score scale times log2(e)
-  // the split: row groups of one sequence and cache head, a workgroup for each or, in the few-row
-  // kernel with shares > 0, so many workgroups with equal shares of all tiles
+  // the split: row groups of one sequence and cache head (of a sequence with max_q queries: others have as
+  // many, the last ones empty), a workgroup for each or, in the few-row kernel with shares > 0, so many
+  // workgroups with equal shares of all row groups' tiles
   int32_t row_groups, shares;
   KvDiv by_row_groups, by_segments;   // row groups; segments of a sequence, heads * row groups
   float* part;             // partial results of the shares
@@ -141,16 +144,20 @@ struct KvPlan {
 constexpr int kKvFewWaves = 4;
 constexpr int kKvShareLeast = 16;  // fewest tiles of a share
 constexpr int kKvManyRows = 128;   // rows of a workgroup of the many-row kernel
-// Most rows of a workgroup of the few-row kernel: 32 where their queries and
-// sums fit the registers.  bf16 at 256 elements does not quite (16 sequences of
-// 20000 tokens, 4 heads, 32 rows, E4M3: 160 us against 125 for groups of 16; 32
-// of 2000, 8 heads, 36 rows: 144 against 85); at 192 the groups of 32 win some
-// (5 x 5 heads, 600 rows over 200 tokens, E2M1: 19 us against 30) and lose some
-// (16 of 5500, 32 rows: 44 against 34).
+// Most rows of a workgroup of the few-row kernel: 32 where groups of 32 gain.
+// bf16 at 256 elements does not (16 sequences of 20000 tokens, 4 heads, 32 rows,
+// E4M3: 160 us against 125 for groups of 16; 32 of 2000, 8 heads, 36 rows: 144
+// against 85).  At 192 they win over short keys (5 x 5 heads, 600 rows over 200
+// tokens, E2M1: 19 us against 30) and lose over long ones (16 of 5500, 32 rows:
+// 44 against 34): their queries and sums do not fit 256 registers (74 spilled
+// for E2M1, 107 for E4M3), and the spilled ones come back at every step.  No
+// rule on the keys' length chooses between the two there.
 constexpr int kv_few_rows(int dtype, int dim) { return dim <= (dtype == NC_BF16 ? 192 : 128) ? 32 : 16; }
 
 // Waves of a SIMD that the few-row kernel is compiled for: queries and sums of
-// nt row tiles, and about 110 registers more.
+// nt row tiles, and about 110 registers more.  An estimate; where it is too low
+// registers spill: 74 and 107 at bf16 192 with 32 rows, 24 at bf16 256 (E4M3, its
+// single tokens too), 2 to 6 at fp32 192 and at fp32 96 with 32 rows.
 constexpr int kv_few_waves(int dtype, int dim, int nt) {
   const int need = (dtype == NC_BF16 ? 1 : 3) * nt * dim / 8 + nt * dim / 4 + 110;
   return need <= 168 ? 3 : need <= 256 ? 2 : 1;

@@ -24,16 +24,24 @@
 //
 // fp32 queries and weights are cut into three bf16 parts of 8 significant bits,
 // exactly; products and sums are fp32.  bf16 calls round the weights to bf16
-// (2^-8 relative, as their output is) and sum them before the rounding.
+// (by 2^-8 at most, as their output is) and sum them before the rounding: one
+// product with the values instead of the three of fp32 calls.  Against the
+// definition the results are then 1.69e-3 of their size apart where weights kept
+// whole would leave the output's own rounding, 1.66e-3 (517 tokens; 262144:
+// 1.644e-3 and 1.643e-3).
 //
 // The waves of a workgroup take turns along the keys, two tiles at a time;
-// their sums meet in LDS.  Long caches are cut over the workgroups, in equal
-// shares of all sequences' tokens, and their sums meet in a second kernel.
+// their sums meet in LDS.  Long caches are cut over the workgroups, in shares
+// that are equal however unequal the lengths are, and their sums meet in a
+// second kernel.
 //
-// Measured: the next token of one sequence, 262144 tokens of 8 heads of 128 in
-// E2M1 (285 MB), 49 us and 6 us for the second kernel (5.8 TB/s; a large copy
-// reaches 5.2); 64 sequences of 1024 .. 8192 tokens 67 and 7 us (331 MB), where
-// the waves wait at every change of sequence; 517 tokens 8 us, of which 5.6 are
+// Measured, the same cache at every call, so that up to 256 MB of it may come
+// from the last-level cache: the next token of one sequence, 262144 tokens of 8
+// heads of 128 in E2M1 (285 MB), 51 us and 6.6 us for the second kernel; 64
+// sequences of 1024 .. 8192 tokens 70 and 7 us (331 MB), where the waves wait at
+// every change of sequence.  On caches that change from call to call both take
+// 64 and 78 us with the launches (4.5 and 4.3 TB/s; a large copy reaches 5.1,
+// reads alone 7.0).  517 tokens take 7.5 us, of which 5.6 are
 // there for 32 tokens already (dependent loads: lengths, table, codes).  Wider
 // steps (four tiles, 170 registers and more) left one wave a SIMD: 110 us.  The
 // second kernel as the last workgroup's task needs a device-wide release from
@@ -471,8 +479,12 @@ __device__ __forceinline__ void kv_store(const KvAttn& a, const KvSpan& sp, int 
 // A segment is one (sequence, head, row group); its length is the tiles of 16
 // keys that the sequence's rows reach, at least 1.  Lengths live on the device,
 // so each workgroup works them out: all segments lie one after the other on a
-// line, and workgroup w takes the tiles [w share, (w + 1) share) of it, however
-// unequal the sequences are.  Whole segments inside a share are finished there;
+// line, and workgroup w takes the tiles [w share, (w + 1) share) of it.  Every
+// sequence has the row groups of max_q queries: groups past its own queries take
+// up line but no time, so the work of the shares is equal where the sequences
+// have about as many queries each (lengths may differ), and not where they differ
+// (one sequence of 64 queries among 31 single tokens, 8192 tokens each, 8 heads
+// of 128 x 4, E2M1: 261 us, and 84 as two calls).  Whole segments inside a share are finished there;
 // the one that began before it goes to partial place 2 w, the one that goes on
 // behind it to place 2 w + 1.
 struct KvReach {
