@@ -17,6 +17,11 @@ Device buffers used by the calls, as torch tensors:
 
 The key/value cache (new_kv_cache, nc_kv_write, nc_kv_read, nc_kv_attention)
 keeps keys and values as MX blocks of E2M1 or E4M3 codes in pages.
+
+MX matrices (new_mx_matrix, nc_mx_write, nc_mx_read) hold a matrix as blocks of
+E2M1, E4M3 or E5M2 codes, laid out for the products nc_mx_matmul and
+nc_mx_linear; nc_act_forward and nc_act_backward keep an activation's inputs in
+them for the backward pass.
 """
 
 import ctypes
@@ -30,7 +35,8 @@ import torch
 from . import _lib
 from ._lib import (NC_BF16, NC_E2M1, NC_E4M3, NC_E5M2, NC_EST_CURRENT, NC_EST_EMA, NC_EST_MAX_WINDOW,  # noqa: F401
                    NC_EST_MOST_RECENT, NC_F32, NC_MX_CEIL, NC_MX_OCP, NC_MX_PLUS1, NC_W_BF16, NC_W_FP16,
-                   NcKvAttn, NcKvCache, NcKvRows, NcPolicy, NcSwampPolicy, NcTensor, NcUpdateTensor)
+                   NC_ACT_GELU, NC_ACT_GELU_TANH, NC_ACT_RELU2, NC_ACT_SILU, NcKvAttn, NcKvCache, NcKvRows, NcMxMatrix,
+                   NcMxOut, NcPlane, NcPolicy, NcSwampPolicy, NcTensor, NcUpdateTensor)
 
 COUNT_FIELDS = ("n_finite", "n_clip", "n_underflow", "n_nonfinite")
 STAT_FIELDS = ("sum_e", "sum_abs_e", "sum_e2", "sum_dir_e", "sum_xe", "sum_x2")
@@ -508,13 +514,13 @@ def _kv_stream(stream, gpu: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _kv_call(cache: KvCache, name: str, call, *args):
-    """The library's call with the cache's GPU as the current one: a default stream's number is 0 on every GPU,
-    and means the current one's."""
-    if torch._C._cuda_getDevice() == cache._gpu:  # torch.cuda.current_device(), for a GPU that is in use
+def _kv_call(at, name: str, call, *args):
+    """The library's call with the GPU of the cache or matrix as the current one: a default stream's number is 0 on
+    every GPU, and means the current one's."""
+    if torch._C._cuda_getDevice() == at._gpu:     # torch.cuda.current_device(), for a GPU that is in use
         status = call(*args)
     else:
-        with torch.cuda.device(cache.device):
+        with torch.cuda.device(at.device):
             status = call(*args)
     if status:
         _check(status, name)
@@ -643,3 +649,266 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
                  q_heads, max_q, max_kv, 1 if causal else 0, window, scale)
     wat, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
     _kv_call(cache, "nc_kv_attention", _lib.load().nc_kv_attention, c, a, code, wat, wn, _kv_stream(stream, cache._gpu))
+
+
+# -- MX matrices and their products ---------------------------------------------
+
+MX_FMT = {"e2m1": NC_E2M1, "e4m3": NC_E4M3, "e5m2": NC_E5M2}
+ACT = {"silu": NC_ACT_SILU, "gelu": NC_ACT_GELU, "gelu_tanh": NC_ACT_GELU_TANH, "relu2": NC_ACT_RELU2}
+_MX_ELEMENT = {torch.float32: (NC_F32, 4), torch.bfloat16: (NC_BF16, 2)}   # code, bytes of an element
+
+
+class MxMatrix:
+    """A matrix [rows, cols] as MX blocks of 32 elements along its rows.
+
+    data is one uint8 tensor of mx_bytes(rows, cols, fmt) bytes or more; another
+    may take its place.  The order of its bytes belongs to the library.  rows,
+    cols and fmt ("e2m1", "e4m3" or "e5m2") are fixed."""
+
+    def __init__(self, data: torch.Tensor, rows: int, cols: int, fmt: str):
+        self._bytes = mx_bytes(rows, cols, fmt)
+        self._rows, self._cols, self._fmt, self._code = int(rows), int(cols), fmt, MX_FMT[fmt]
+        self.data = data
+
+    rows, cols, fmt = (property(attrgetter(name)) for name in ("_rows", "_cols", "_fmt"))
+    device, data = (property(attrgetter(name)) for name in ("_device", "_data"))
+
+    @data.setter
+    def data(self, data: torch.Tensor):
+        if data.dtype != torch.uint8 or data.dim() != 1 or data.numel() < self._bytes or not data.is_contiguous():
+            raise ValueError(f"data: shape {tuple(data.shape)} of {data.dtype}, expected contiguous torch.uint8 of "
+                             f"{self._bytes} bytes")
+        self._data, self._at, self._held, self._device = data, data.data_ptr(), data.numel(), data.device
+        self._gpu = data.device.index if data.device.type == "cuda" else None
+        self._descriptor = NcMxMatrix(self._at if self._bytes else None, self._rows, self._cols, self._code, 0)
+
+    @property
+    def descriptor(self) -> NcMxMatrix:
+        """What the calls pass on.  A tensor may be resized in place, so data is looked at every time."""
+        d = self._data
+        if d.data_ptr() != self._at or d.numel() != self._held:
+            self.data = d
+        return self._descriptor
+
+
+def mx_bytes(rows: int, cols: int, fmt: str) -> int:
+    """Bytes of a matrix's data."""
+    if fmt not in MX_FMT:
+        raise ValueError(f"fmt {fmt!r}: one of {sorted(MX_FMT)}")
+    if not 0 <= min(rows, cols) <= max(rows, cols) <= _I32_MAX:
+        raise ValueError(f"rows {rows}, cols {cols}: 0 to 2^31 - 1 each")
+    n = int(_lib.load().nc_mx_bytes(rows, cols, MX_FMT[fmt]))
+    if n == 0 and rows and cols:
+        raise ValueError(f"rows {rows}, cols {cols}: (rows / 32) * (cols / 256), each rounded up, stays below 2^24")
+    return n
+
+
+def new_mx_matrix(rows: int, cols: int, fmt: str = "e2m1", device="cuda") -> MxMatrix:
+    """A matrix of zeros."""
+    return MxMatrix(torch.zeros(mx_bytes(rows, cols, fmt), dtype=torch.uint8, device=device), rows, cols, fmt)
+
+
+def _plane(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, dev: torch.device, out: bool = False) -> NcPlane:
+    """The call's view of a [rows, cols] tensor with adjacent elements; any row stride, without overlap where it is
+    written."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} of {t.dtype} on {t.device}, expected {tuple(shape)} of "
+                         f"{dtype} on {dev}")
+    stride, one = t.stride()
+    rows, cols = shape
+    if rows < 2:                                 # torch gives an axis of length 1 any stride
+        stride = cols
+    if (cols > 1 and one != 1) or (out and stride < cols):
+        raise ValueError(f"{name}: strides {t.stride()}: rows of adjacent elements"
+                         f"{' that do not overlap' if out else ''} expected")
+    return NcPlane(t.data_ptr(), stride)
+
+
+def _element(t: torch.Tensor, name: str) -> int:
+    code, _ = _MX_ELEMENT.get(t.dtype, (None, 0))
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype} (float32 or bfloat16 expected)")
+    return code
+
+
+def _on(*matrices: MxMatrix):
+    """One device for all, a GPU."""
+    dev = matrices[0]._device
+    for m in matrices[1:]:
+        if m._device != dev:
+            raise ValueError(f"matrices on {dev} and {m._device}")
+    if matrices[0]._gpu is None:
+        raise ValueError("device tensor expected (no CPU path)")
+    return dev
+
+
+def _rule(rule) -> int:
+    if rule not in MX_RULE:
+        raise ValueError(f"rule {rule!r}: one of {sorted(MX_RULE)}")
+    return MX_RULE[rule]
+
+
+def nc_mx_write(x: torch.Tensor, m: Optional[MxMatrix] = None, t: Optional[MxMatrix] = None, rule="ceil", stream=None):
+    """Quantise x [rows, cols] (fp32 or bf16, any row stride) into m, with blocks along its rows, and into t, the
+    transposed matrix [cols, rows] with blocks down its columns; one of them or, from one read of x, both."""
+    code, r = _element(x, "x"), _rule(rule)
+    any_ = m if m is not None else t
+    if any_ is None:
+        raise ValueError("m or t: one matrix at least")
+    md, td = (None if q is None else q.descriptor for q in (m, t))   # first: they look at data anew
+    shape = (m.rows, m.cols) if m is not None else (t.cols, t.rows)
+    if m is not None and t is not None and ((t.cols, t.rows) != shape or t.fmt != m.fmt):
+        raise ValueError(f"t: {t.rows} x {t.cols} of {t.fmt}, expected {m.cols} x {m.rows} of {m.fmt}")
+    dev = _on(*(q for q in (m, t) if q is not None))
+    _kv_call(any_, "nc_mx_write", _lib.load().nc_mx_write, md, td, _plane(x, "x", shape, x.dtype, dev), code, r,
+             _kv_stream(stream, any_._gpu))
+
+
+def nc_mx_read(m: MxMatrix, out: torch.Tensor, stream=None):
+    """The matrix's values, as fp32 or bf16 [rows, cols]."""
+    code, d = _element(out, "out"), m.descriptor
+    y = _plane(out, "out", (m.rows, m.cols), out.dtype, _on(m), out=True)
+    _kv_call(m, "nc_mx_read", _lib.load().nc_mx_read, d, y, code, _kv_stream(stream, m._gpu))
+
+
+def mx_workspace_bytes(rows: int, w: MxMatrix, fmt: Optional[str] = None) -> int:
+    if fmt is not None and fmt not in MX_FMT:
+        raise ValueError(f"fmt {fmt!r}: one of {sorted(MX_FMT)}")
+    if not 0 <= rows <= _I32_MAX:
+        raise ValueError(f"rows {rows}: 0 to 2^31 - 1")
+    return int(_lib.load().nc_mx_workspace_bytes(w.descriptor, rows, -1 if fmt is None else MX_FMT[fmt]))
+
+
+def new_mx_workspace(rows: int, w: MxMatrix, fmt: Optional[str] = None) -> torch.Tensor:
+    """Device workspace for products of w with this many rows or fewer: for nc_mx_matmul, or with `fmt` for
+    nc_mx_linear of that format.  Calls that run concurrently need workspaces of their own."""
+    return torch.empty(max(mx_workspace_bytes(rows, w, fmt), 16), dtype=torch.uint8, device=w.device)
+
+
+def _mx_out(out: torch.Tensor, rows: int, w: MxMatrix, bias: Optional[torch.Tensor], accumulate: bool) -> NcMxOut:
+    code = _element(out, "out")
+    p = _plane(out, "out", (rows, w.rows), out.dtype, w._device, out=True)
+    at = None
+    if bias is not None:
+        if bias.dtype is not out.dtype or bias.shape != (w.rows,) or bias.device != w._device or not bias.is_contiguous():
+            raise ValueError(f"bias: shape {tuple(bias.shape)} of {bias.dtype} on {bias.device}, expected contiguous "
+                             f"({w.rows},) of {out.dtype} on {w._device}")
+        at = bias.data_ptr()
+    return NcMxOut(p.data, p.stride, code, 1 if accumulate else 0, at)
+
+
+def _mx_ws(ws: Optional[torch.Tensor], need: int, w: MxMatrix, stream):
+    """Pointer and size of the workspace; where none is given and some is needed, one from torch on the call's own
+    stream: freed memory is handed out again in that stream's order."""
+    if ws is not None:
+        if ws.dtype is not torch.uint8 or ws.device != w._device or not ws.is_contiguous():
+            raise ValueError(f"ws: dtype {ws.dtype} on {ws.device}, expected contiguous torch.uint8 on {w._device}")
+    elif need:
+        on = torch.cuda.current_stream(w._device) if stream is None else (
+            stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=w._device))
+        with torch.cuda.stream(on):
+            ws = torch.empty(need, dtype=torch.uint8, device=w._device)
+    return (None, 0, None) if ws is None else (ws.data_ptr(), ws.numel(), ws)
+
+
+def nc_mx_matmul(a: MxMatrix, b: MxMatrix, out: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                 accumulate: bool = False, ws: Optional[torch.Tensor] = None, stream=None):
+    """out = a b^T (+ bias) (+ out with accumulate): a [rows, k], b [n, k], out [rows, n] fp32 or bf16, bias [n] of
+    the same type.  The formats may differ."""
+    ad, bd = a.descriptor, b.descriptor
+    if a.cols != b.cols:
+        raise ValueError(f"a: {a.cols} columns, b has {b.cols}")
+    _on(b, a)
+    o = _mx_out(out, a.rows, b, bias, accumulate)
+    lib = _lib.load()
+    at, n, held = _mx_ws(ws, lib.nc_mx_workspace_bytes(bd, a.rows, -1) if ws is None else 0, b, stream)
+    _kv_call(b, "nc_mx_matmul", lib.nc_mx_matmul, ad, bd, o, at, n, _kv_stream(stream, b._gpu))
+
+
+def nc_mx_linear(x: torch.Tensor, w: MxMatrix, out: torch.Tensor, fmt: str = "e4m3", rule="ceil",
+                 bias: Optional[torch.Tensor] = None, accumulate: bool = False, ws: Optional[torch.Tensor] = None,
+                 stream=None):
+    """out = q(x) w^T (+ bias) (+ out): x [rows, k] fp32 or bf16, quantised to `fmt` on the way with blocks along its
+    rows; w [n, k]; out [rows, n] fp32 or bf16."""
+    code, r = _element(x, "x"), _rule(rule)
+    if fmt not in MX_FMT:
+        raise ValueError(f"fmt {fmt!r}: one of {sorted(MX_FMT)}")
+    wd = w.descriptor
+    dev = _on(w)
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, {w.cols})")
+    rows = x.shape[0]
+    p = _plane(x, "x", (rows, w.cols), x.dtype, dev)
+    if rows > _I32_MAX:
+        raise ValueError(f"x: {rows} rows, at most 2^31 - 1")
+    o = _mx_out(out, rows, w, bias, accumulate)
+    lib = _lib.load()
+    at, n, held = _mx_ws(ws, lib.nc_mx_workspace_bytes(wd, rows, MX_FMT[fmt]) if ws is None else 0, w, stream)
+    _kv_call(w, "nc_mx_linear", lib.nc_mx_linear, p, rows, code, MX_FMT[fmt], r, wd, o, at, n, _kv_stream(stream, w._gpu))
+
+
+# -- activations that keep their inputs in 8 or 4 bits ----------------------------
+
+
+def _act(act) -> int:
+    if act not in ACT:
+        raise ValueError(f"act {act!r}: one of {sorted(ACT)}")
+    return ACT[act]
+
+
+def _alike(up_q: MxMatrix, gate_q: MxMatrix):
+    if (up_q.rows, up_q.cols, up_q.fmt) != (gate_q.rows, gate_q.cols, gate_q.fmt):
+        raise ValueError(f"up_q: {up_q.rows} x {up_q.cols} of {up_q.fmt}, expected {gate_q.rows} x {gate_q.cols} of "
+                         f"{gate_q.fmt}")
+
+
+class _Gpu:
+    """The device of a call that has no matrix."""
+
+    def __init__(self, device: torch.device):
+        self.device = self._device = device
+        self._gpu = device.index if device.type == "cuda" else None
+
+
+def nc_act_forward(gate: torch.Tensor, up: Optional[torch.Tensor], y: torch.Tensor, gate_q: Optional[MxMatrix] = None,
+                   up_q: Optional[MxMatrix] = None, act="silu", rule="ceil", stream=None):
+    """y = f(gate) * up, or f(gate) where up is None; gate and up [rows, cols] fp32 or bf16 (any row stride: halves of
+    one projection will do).  gate_q and up_q, matrices of that shape, keep them for nc_act_backward; without them
+    nothing is kept.  act: "silu", "gelu", "gelu_tanh" or "relu2"."""
+    f, code, r = _act(act), _element(gate, "gate"), _rule(rule)
+    if gate.dim() != 2:
+        raise ValueError(f"gate: shape {tuple(gate.shape)}, expected (rows, cols)")
+    shape, dt = gate.shape, gate.dtype
+    if (up_q is not None) if gate_q is None else (up_q is None) != (up is None):
+        raise ValueError("up_q goes with up and gate_q")
+    if gate_q is None:
+        mx_bytes(*shape, "e4m3")                 # the sizes that a call takes
+    gd, ud = (None if q is None else q.descriptor for q in (gate_q, up_q))
+    at = gate_q if gate_q is not None else _Gpu(gate.device)
+    dev = _on(*(q for q in (at, up_q) if q is not None))
+    if gate_q is not None and (gate_q.rows, gate_q.cols) != tuple(shape):
+        raise ValueError(f"gate_q: {gate_q.rows} x {gate_q.cols}, expected {shape[0]} x {shape[1]}")
+    if up_q is not None:
+        _alike(up_q, gate_q)
+    gp, yp = _plane(gate, "gate", shape, dt, dev), _plane(y, "y", shape, dt, dev, out=True)
+    up_ = None if up is None else _plane(up, "up", shape, dt, dev)
+    _kv_call(at, "nc_act_forward", _lib.load().nc_act_forward, f, *shape, gp, up_, yp, code, gd, ud, r,
+             _kv_stream(stream, at._gpu))
+
+
+def nc_act_backward(dy: torch.Tensor, gate_q: MxMatrix, up_q: Optional[MxMatrix], dgate: torch.Tensor,
+                    dup: Optional[torch.Tensor] = None, act="silu", y: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of nc_act_forward from what it kept: dgate = dy u f'(g), dup = dy f(g) (with up_q), g and u the
+    kept values; and, where y is given, y = f(g) u again, for the gradient of the weights it was multiplied with."""
+    f, code, dt = _act(act), _element(dy, "dy"), dy.dtype
+    if (up_q is None) != (dup is None):
+        raise ValueError("dup goes with up_q")
+    gd, ud = gate_q.descriptor, None if up_q is None else up_q.descriptor
+    dev = _on(*(q for q in (gate_q, up_q) if q is not None))
+    if up_q is not None:
+        _alike(up_q, gate_q)
+    shape = (gate_q.rows, gate_q.cols)
+    dyp, dgp = _plane(dy, "dy", shape, dt, dev), _plane(dgate, "dgate", shape, dt, dev, out=True)
+    dup_, yp = (None if t is None else _plane(t, n, shape, dt, dev, out=True) for t, n in ((dup, "dup"), (y, "y")))
+    _kv_call(gate_q, "nc_act_backward", _lib.load().nc_act_backward, f, dyp, code, gd, ud, dgp, dup_, yp,
+             _kv_stream(stream, gate_q._gpu))

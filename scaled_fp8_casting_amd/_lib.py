@@ -83,12 +83,26 @@ class NcKvAttn(ctypes.Structure):
                                        "window")] + [("scale", ctypes.c_float)]
 
 
+class NcMxMatrix(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("rows", c_int64), ("cols", c_int64), ("fmt", c_int32), ("reserved", c_int32)]
+
+
+class NcPlane(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("stride", c_int64)]
+
+
+class NcMxOut(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("stride", c_int64), ("dtype", c_int32), ("accumulate", c_int32), ("bias", c_void_p)]
+
+
 NC_W_BF16, NC_W_FP16 = 0, 1
+NC_ACT_SILU, NC_ACT_GELU, NC_ACT_GELU_TANH, NC_ACT_RELU2 = range(4)
 
 EXPORTS = ("nc_amax", "nc_scale_update", "nc_cast_tensor", "nc_cast_tensor_static", "nc_cast_tensor_sr", "nc_cast_mx", "nc_dequant",
            "nc_cast_stats", "nc_workspace_bytes", "nc_status_string", "nc_swamp_workspace_bytes",
            "nc_swamp_watch", "nc_swamp_window", "nc_kv_cache_bytes", "nc_kv_write", "nc_kv_read", "nc_kv_attention",
-           "nc_kv_workspace_bytes")
+           "nc_kv_workspace_bytes", "nc_mx_bytes", "nc_mx_write", "nc_mx_read", "nc_mx_matmul", "nc_mx_linear",
+           "nc_mx_workspace_bytes", "nc_act_forward", "nc_act_backward")
 
 _lib = None
 
@@ -129,12 +143,24 @@ def load():
     lib.nc_kv_attention.argtypes = [C, POINTER(NcKvAttn), c_int32, c_void_p, c_size_t, c_void_p]
     lib.nc_kv_workspace_bytes.argtypes = [C, c_int32, c_int32, c_int32, c_int32, c_int32]
     lib.nc_kv_workspace_bytes.restype = c_size_t
+    M, P = POINTER(NcMxMatrix), POINTER(NcPlane)
+    lib.nc_mx_bytes.argtypes = [c_int64, c_int64, c_int32]
+    lib.nc_mx_bytes.restype = c_size_t
+    lib.nc_mx_write.argtypes = [M, M, P, c_int32, c_int32, c_void_p]
+    lib.nc_mx_read.argtypes = [M, P, c_int32, c_void_p]
+    lib.nc_mx_matmul.argtypes = [M, M, POINTER(NcMxOut), c_void_p, c_size_t, c_void_p]
+    lib.nc_mx_linear.argtypes = [P, c_int64, c_int32, c_int32, c_int32, M, POINTER(NcMxOut), c_void_p, c_size_t, c_void_p]
+    lib.nc_mx_workspace_bytes.argtypes = [M, c_int64, c_int32]
+    lib.nc_mx_workspace_bytes.restype = c_size_t
+    lib.nc_act_forward.argtypes = [c_int32, c_int64, c_int64, P, P, P, c_int32, M, M, c_int32, c_void_p]
+    lib.nc_act_backward.argtypes = [c_int32, P, c_int32, M, M, P, P, P, c_void_p]
     lib.nc_workspace_bytes.argtypes = [T, c_int32]
     lib.nc_workspace_bytes.restype = c_size_t
     lib.nc_status_string.argtypes = [c_int32]
     lib.nc_status_string.restype = c_char_p
     for name in ("nc_amax", "nc_scale_update", "nc_cast_tensor", "nc_cast_tensor_static", "nc_cast_tensor_sr", "nc_cast_mx", "nc_dequant",
-                 "nc_cast_stats", "nc_swamp_watch", "nc_swamp_window", "nc_kv_write", "nc_kv_read", "nc_kv_attention"):
+                 "nc_cast_stats", "nc_swamp_watch", "nc_swamp_window", "nc_kv_write", "nc_kv_read", "nc_kv_attention", "nc_mx_write",
+                 "nc_mx_read", "nc_mx_matmul", "nc_mx_linear", "nc_act_forward", "nc_act_backward"):
         getattr(lib, name).restype = c_int32
     _lib = lib
     return lib

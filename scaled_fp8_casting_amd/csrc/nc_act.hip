@@ -1,0 +1,187 @@
+// Activations that keep their inputs as MX blocks, and their gradients from what
+// was kept.
+//
+//   forward:  y = f(gate) up;  gate and up quantised
+//   backward: dgate = dy up f'(gate), dup = dy f(gate), and y again where wanted,
+//             with gate and up as they were kept
+//
+// f: silu z s(z) with s(z) = 1 / (1 + e^-z); gelu z Phi(z); gelu_tanh
+// z s(2 c (z + 0.044715 z^3)), c = sqrt(2 / pi) (0.5 (1 + tanh u) = s(2 u));
+// relu2 max(z, 0)^2.  Derivatives: s + z s (1 - s); Phi + z phi(z); s + z s (1 - s)
+// 2 c (1 + 3 * 0.044715 z^2); 2 max(z, 0).  All in fp32; z = -inf gives NaN where
+// the formula does (-inf times 0).
+//
+// Each byte moves once, so HBM bandwidth bounds them.
+#include <cfloat>
+
+#include "nc_mx.h"
+
+namespace nc {
+namespace {
+
+// z cut to [-most, most]: where a factor next to it is 0 already, infinities and
+// overflows would make NaN of the product.
+__device__ __forceinline__ float within(float z, float most) { return fminf(fmaxf(z, -most), most); }
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+template <int ACT> __device__ __forceinline__ void act_of(float z, float& f, float& df) {
+  if constexpr (ACT == NC_ACT_SILU) {
+    const float s = sigmoid(z);
+    f = z * s;
+    df = s * (1.0f + within(z, FLT_MAX) * (1.0f - s));
+  } else if constexpr (ACT == NC_ACT_GELU) {
+    const float phi = 0.5f * erfcf(z * -0.70710678118654752f);
+    f = z * phi;
+    df = phi + within(z, FLT_MAX) * (expf(-0.5f * z * z) * 0.39894228040143268f);
+  } else if constexpr (ACT == NC_ACT_GELU_TANH) {
+    constexpr float c2 = 1.5957691216057308f, k = 0.044715f;   // 2 sqrt(2 / pi)
+    const float n = within(z, 16.0f);            // s is 0 or 1 from there on
+    const float s = z == z ? sigmoid(c2 * (n + k * n * n * n)) : z;
+    f = z * s;
+    df = s + n * s * (1.0f - s) * (c2 * (1.0f + 3.0f * k * n * n));
+  } else {
+    const float r = z > 0.0f ? z : (z != z ? z : 0.0f);
+    f = r * r;
+    df = 2.0f * r;
+  }
+}
+
+template <int DT> __device__ __forceinline__ void floats(const Eight<DT>& x, float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(bits_of<DT>(x, i));
+}
+template <int DT> __device__ __forceinline__ const uint8_t* row_of(const Plane<const void*>& x, int64_t row) {
+  return static_cast<const uint8_t*>(x.p) + row * x.stride * In<DT>::BYTES;
+}
+template <int DT> __device__ __forceinline__ uint8_t* row_of(const Plane<void*>& x, int64_t row) {
+  return static_cast<uint8_t*>(x.p) + row * x.stride * In<DT>::BYTES;
+}
+
+template <int ACT, int FMT, int DT, bool GATED>
+NC_STREAM_KERNEL act_forward(ActForward a) {
+  const MxLane at(a.gate_q);
+  const bool there = at.row < a.gate_q.rows;
+  Eight<DT> g[4], u[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int64_t left = there ? a.gate_q.cols - at.col(s) : 0;
+    g[s] = load8<DT>(row_of<DT>(a.gate, at.row), at.col(s), left);
+    if constexpr (GATED) u[s] = load8<DT>(row_of<DT>(a.up, at.row), at.col(s), left);
+  }
+  if (a.gate_q.codes != nullptr) {
+    uint32_t sg = 0, su = 0;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      uint32_t sb;
+      put_codes<FMT>(a.gate_q.codes + at.codes<FMT>(s), encode_quad<FMT, DT>(g[s], a.rule, sb));
+      sg |= sb << (8 * s);
+      if constexpr (GATED) {
+        put_codes<FMT>(a.up_q.codes + at.codes<FMT>(s), encode_quad<FMT, DT>(u[s], a.rule, sb));
+        su |= sb << (8 * s);
+      }
+    }
+    if ((at.q & 3) == 0) {
+      *reinterpret_cast<uint32_t*>(a.gate_q.scales + at.scales()) = sg;
+      if constexpr (GATED) *reinterpret_cast<uint32_t*>(a.up_q.scales + at.scales()) = su;
+    }
+  }
+  if (!there) return;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    float z[8], w[8], y[8];
+    floats<DT>(g[s], z);
+    if constexpr (GATED) floats<DT>(u[s], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f, df;
+      act_of<ACT>(z[i], f, df);
+      y[i] = GATED ? f * w[i] : f;
+    }
+    store8<DT>(row_of<DT>(a.y, at.row), at.col(s), a.gate_q.cols - at.col(s), eight_of<DT>(y));
+  }
+}
+
+template <int ACT, int FMT, int DT, bool GATED>
+NC_STREAM_KERNEL act_backward(ActBackward a) {
+  const MxLane at(a.gate_q);
+  if (at.row >= a.gate_q.rows) return;
+  Eight<DT> dy[4];
+  u32x2 g[4], u[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    dy[s] = load8<DT>(row_of<DT>(a.dy, at.row), at.col(s), a.gate_q.cols - at.col(s));
+    g[s] = get_codes<FMT>(a.gate_q.codes + at.codes<FMT>(s));
+    if constexpr (GATED) u[s] = get_codes<FMT>(a.up_q.codes + at.codes<FMT>(s));
+  }
+  const uint32_t sg = *reinterpret_cast<const uint32_t*>(a.gate_q.scales + at.scales());
+  uint32_t su = 0;
+  if constexpr (GATED) su = *reinterpret_cast<const uint32_t*>(a.up_q.scales + at.scales());
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int64_t left = a.gate_q.cols - at.col(s);
+    float d[8], z[8], w[8], dz[8], dw[8], y[8];
+    floats<DT>(dy[s], d);
+    decode8<FMT>(g[s], (sg >> (8 * s)) & 255u, z);
+    if constexpr (GATED) decode8<FMT>(u[s], (su >> (8 * s)) & 255u, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f, df;
+      act_of<ACT>(z[i], f, df);
+      dz[i] = GATED ? d[i] * w[i] * df : d[i] * df;
+      dw[i] = d[i] * f;
+      y[i] = GATED ? f * w[i] : f;
+    }
+    store8<DT>(row_of<DT>(a.dgate, at.row), at.col(s), left, eight_of<DT>(dz));
+    if constexpr (GATED) store8<DT>(row_of<DT>(a.dup, at.row), at.col(s), left, eight_of<DT>(dw));
+    if (a.y.p != nullptr) store8<DT>(row_of<DT>(a.y, at.row), at.col(s), left, eight_of<DT>(y));
+  }
+}
+
+template <int ACT, int FMT, typename Fn> hipError_t by_dtype(int dtype, Fn fn) {
+  return dtype == NC_BF16 ? fn.template operator()<ACT, FMT, NC_BF16>() : fn.template operator()<ACT, FMT, NC_F32>();
+}
+template <int ACT, typename Fn> hipError_t by_format(int fmt, int dtype, Fn fn) {
+  return fmt == NC_E2M1 ? by_dtype<ACT, NC_E2M1>(dtype, fn)
+       : fmt == NC_E4M3 ? by_dtype<ACT, NC_E4M3>(dtype, fn) : by_dtype<ACT, NC_E5M2>(dtype, fn);
+}
+template <typename Fn> hipError_t by_act(int act, int fmt, int dtype, Fn fn) {
+  switch (act) {
+    case NC_ACT_SILU: return by_format<NC_ACT_SILU>(fmt, dtype, fn);
+    case NC_ACT_GELU: return by_format<NC_ACT_GELU>(fmt, dtype, fn);
+    case NC_ACT_GELU_TANH: return by_format<NC_ACT_GELU_TANH>(fmt, dtype, fn);
+    case NC_ACT_RELU2: return by_format<NC_ACT_RELU2>(fmt, dtype, fn);
+  }
+  return hipErrorInvalidValue;
+}
+
+uint32_t grid_of(const MxMat& m) { return (uint32_t)m.strips * (uint32_t)m.chunks; }
+
+struct Forward {
+  const ActForward& a;
+  hipStream_t stream;
+  template <int ACT, int FMT, int DT> hipError_t operator()() const {
+    if (a.up.p != nullptr) act_forward<ACT, FMT, DT, true><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
+    else act_forward<ACT, FMT, DT, false><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
+    return hipGetLastError();
+  }
+};
+struct Backward {
+  const ActBackward& a;
+  hipStream_t stream;
+  template <int ACT, int FMT, int DT> hipError_t operator()() const {
+    if (a.up_q.codes != nullptr) act_backward<ACT, FMT, DT, true><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
+    else act_backward<ACT, FMT, DT, false><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
+    return hipGetLastError();
+  }
+};
+
+}  // namespace
+
+hipError_t launch_act_forward(const ActForward& a, int act, int fmt, int dtype, hipStream_t stream) {
+  return by_act(act, fmt, dtype, Forward{a, stream});
+}
+hipError_t launch_act_backward(const ActBackward& a, int act, int fmt, int dtype, hipStream_t stream) {
+  return by_act(act, fmt, dtype, Backward{a, stream});
+}
+
+}  // namespace nc

@@ -1,0 +1,152 @@
+// Products of operands of MX blocks: what the product kernels share.
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 x 64 by 64 x 32 codes and
+// applies each block's scale on the way.  Of eight neighbouring columns it keeps
+// the products' bits down to 2^-13 of the largest one's binade; the groups of
+// eight, blocks and steps meet in fp32 (measured with single products at every
+// distance).  Two E2M1 operands never reach below that and are summed exactly (no
+// difference from 64 bits over 4096 columns of normal and heavy-tailed data).
+// With an 8-bit operand 1.3e-5 of the result's size is lost for normal data and up
+// to 1e-4 for heavy tails, far inside the rounding of a bf16 result (1.7e-3) but
+// not of an fp32 one.  So products with fp32 results and an 8-bit operand convert
+// the codes to bf16 (exact: at most four significant bits; values below 2^-133 are
+// rounded) and take four 32x32x16 bf16 products in place of one, with exact
+// products and fp32 sums.
+#pragma once
+
+#include "nc_mx.h"
+
+namespace nc {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+// What the instruction calls a format.
+constexpr int mx_code(int fmt) { return fmt == NC_E2M1 ? 4 : fmt == NC_E5M2 ? 1 : 0; }
+
+// A lane's part of an operand of 32 rows and 64 columns.
+template <int FMT> struct MxFrag { u32x4 w[FMT == NC_E2M1 ? 1 : 2]; };
+
+template <int FMT> __device__ __forceinline__ MxFrag<FMT> mx_frag(const uint8_t* step, int lane) {
+  MxFrag<FMT> f;
+#pragma unroll
+  for (int h = 0; h < (FMT == NC_E2M1 ? 1 : 2); ++h) f.w[h] = *reinterpret_cast<const u32x4*>(step + h * 1024 + lane * 16);
+  return f;
+}
+
+template <int FMT> __device__ __forceinline__ i32x8_t mx_operand(const MxFrag<FMT>& f) {
+  if constexpr (FMT == NC_E2M1)
+    return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(f.w[0], f.w[0], 0, 1, 2, 3, -1, -1, -1, -1));
+  else
+    return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(f.w[0], f.w[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// acc[row of a][row of b] += a b^T over 64 columns; byte S of sa and sb: the
+// scales of the lane's block.  Register i of lane l is row 8 (i / 4) + 4 (l / 32)
+// + i % 4, column l % 32.
+template <int FA, int FB, int S>
+__device__ __forceinline__ f32x16_t mx_mma(const MxFrag<FA>& a, const MxFrag<FB>& b, const f32x16_t& acc, uint32_t sa, uint32_t sb) {
+  constexpr int CA = mx_code(FA), CB = mx_code(FB);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand<FA>(a), mx_operand<FB>(b), acc, CA, CB, S,
+                                                         (int)sa, S, (int)sb);
+}
+
+// An operand as bf16: four products' worth.  Both operands bring the columns in
+// the 8-bit formats' order -- product i of lane r + 32 g: elements 8 i .. 8 i + 7
+// of the lane's 32, columns 16 g + .. for i < 2 and 32 + 16 g + .. above -- so an
+// E2M1 lane swaps its second 16 elements for the other half's first.
+struct MxWide { u32x4 w[4]; };
+
+template <int FMT> __device__ __forceinline__ MxWide mx_widen(const MxFrag<FMT>& f, uint32_t s0, uint32_t s1) {
+  const float s[2] = {mx_scale(s0), mx_scale(s1)};
+  MxWide v;
+  if constexpr (FMT == NC_E2M1) {
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(f.w[0].x, f.w[0].z, false, false));
+    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(f.w[0].y, f.w[0].w, false, false));
+    const uint32_t c[4] = {x.x, y.x, x.y, y.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v.w[i][j] = mx_pair<FMT>(u32x2{c[i], 0u}, s[i / 2], j);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v.w[i][j] = mx_pair<FMT>(u32x2{f.w[i / 2][2 * (i % 2)], f.w[i / 2][2 * (i % 2) + 1]}, s[i / 2], j);
+  }
+  return v;
+}
+
+__device__ __forceinline__ f32x16_t mx_mma_wide(const MxWide& a, const MxWide& b, f32x16_t acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a.w[i]), __builtin_bit_cast(bf16x8_t, b.w[i]), acc, 0, 0, 0);
+  return acc;
+}
+
+// A lane's scales of a chunk and those of the lane 32 further on: what widening
+// needs of both blocks, block 0's first.
+struct MxScales { uint32_t own, block0, block1; };
+template <bool WIDE> __device__ __forceinline__ MxScales mx_scales(uint32_t own, int lane) {
+  MxScales s = {own, 0u, 0u};
+  if constexpr (WIDE) {
+    const uint32_t other = (uint32_t)__shfl_xor((int)own, 32);
+    s.block0 = lane < 32 ? own : other;
+    s.block1 = lane < 32 ? other : own;
+  }
+  return s;
+}
+
+// One result: bias, what is there already, rounding to out's type.
+__device__ __forceinline__ float mx_bias(const MxProduct& p, int64_t col) {
+  if (p.bias == nullptr) return 0.0f;
+  return p.out_dtype == NC_BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.bias)[col] << 16)
+                                : static_cast<const float*>(p.bias)[col];
+}
+
+// Four neighbouring results of a row, `left` of them inside the matrix.
+__device__ __forceinline__ void mx_store4(const MxProduct& p, int64_t row, int64_t col, int64_t left, const float (&y)[4]) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = y[i] + (i < left ? mx_bias(p, col + i) : 0.0f);
+  const int64_t at = row * p.out_stride + col;
+  if (p.out_dtype == NC_BF16) {
+    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+    if (left >= 4) {
+      u32x2 w;
+      if (p.accumulate) {
+        __builtin_memcpy(&w, o, 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+      }
+      w = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      __builtin_memcpy(o, &w, 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) {
+          if (p.accumulate) v[i] += __uint_as_float((uint32_t)o[i] << 16);
+          o[i] = (uint16_t)bf16_pair(v[i], 0.0f);
+        }
+    }
+  } else {
+    float* o = static_cast<float*>(p.out) + at;
+    if (left >= 4) {
+      float w[4];
+      if (p.accumulate) {
+        __builtin_memcpy(w, o, 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += w[i];
+      }
+      __builtin_memcpy(o, v, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) o[i] = p.accumulate ? o[i] + v[i] : v[i];
+    }
+  }
+}
+
+}  // namespace nc
