@@ -315,6 +315,7 @@ hipError_t launch_mx_write(const MxMat* m, const MxMat* t, int fmt, const Plane<
                            hipStream_t stream);
 hipError_t launch_mx_read(const MxMat& m, int fmt, const Plane<void*>& y, int dtype, hipStream_t stream);
 hipError_t launch_mx_few(const MxProduct& p, int fa, int fb, hipStream_t stream);
+hipError_t launch_mx_many(const MxProduct& p, int fa, int fb, int w, hipStream_t stream);   // tiles of 64 w results a side
 
 struct ActForward {
   Plane<const void*> gate, up;   // up.p null: no gate

@@ -74,9 +74,45 @@ void set_out(MxProduct& p, const nc_mx_out* o) {
   p.accumulate = o->accumulate != 0;
 }
 
-nc_status product(const MxProduct& p, int32_t fa, int32_t fb, hipStream_t stream) {
-  if ((int64_t)p.a.strips * p.b.strips > kMostTiles / 2) return NC_E_ARG;
-  return hip_status(launch_mx_few(p, fa, fb, stream));
+// How a product is cut up.
+struct MxPlan {
+  int w;             // tiles of 64 w results a side; 0: the few-row kernel
+  int32_t splits;    // of the columns
+};
+
+constexpr int64_t kUnits = 256;                  // compute units
+constexpr int64_t kMostSplitTiles = 2 * kUnits;  // tiles of 128 that the card holds at once
+constexpr int64_t kSplitChunks = 4;              // fewest chunks of a split
+
+MxPlan plan_of(int64_t rows_a, int64_t rows_b, int64_t chunks, bool wide) {
+  MxPlan p = {0, 1};
+  if (rows_a <= kMxRows) return p;
+  const auto tiles = [&](int64_t side) { return ((rows_a + side - 1) / side) * ((rows_b + side - 1) / side); };
+  p.w = !wide && tiles(256) >= kUnits * 3 / 4 ? 4 : 2;
+  if (p.w == 2) p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kMostSplitTiles / tiles(128), chunks / kSplitChunks));
+  return p;
+}
+
+size_t part_bytes(int64_t rows_a, int64_t rows_b, int32_t splits) { return splits > 1 ? round256((size_t)(rows_a * rows_b) * 4 * splits) : 0; }
+
+// For every plan of so many or fewer rows: no more than kMostSplitTiles tiles of
+// 128 x 128, nor more splits than chunks allow.
+size_t most_part_bytes(int64_t rows_a, int64_t rows_b, int64_t chunks) {
+  const int64_t splits = std::min<int64_t>(kMostSplitTiles, chunks / kSplitChunks);
+  if (rows_a <= kMxRows || splits < 2) return 0;
+  return round256((size_t)std::min<double>((double)kMostSplitTiles * 128 * 128 * 4, (double)rows_a * (double)rows_b * 4 * (double)splits));
+}
+
+nc_status product(MxProduct& p, int32_t fa, int32_t fb, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const MxPlan plan = plan_of(p.a.rows, p.b.rows, p.b.chunks, p.out_dtype == NC_F32 && (fa != NC_E2M1 || fb != NC_E2M1));
+  p.splits = plan.splits;
+  p.part = (float*)ws;
+  if (part_bytes(p.a.rows, p.b.rows, plan.splits) > ws_bytes) return NC_E_WORKSPACE;
+  if (plan.w == 0) {
+    if ((int64_t)p.a.strips * p.b.strips > kMostTiles / 2) return NC_E_ARG;
+    return hip_status(launch_mx_few(p, fa, fb, stream));
+  }
+  return hip_status(launch_mx_many(p, fa, fb, plan.w, stream));
 }
 
 }  // namespace
@@ -114,8 +150,9 @@ nc_status nc_mx_read(const nc_mx_matrix* m, const nc_plane* y, nc_dtype dtype, v
 
 size_t nc_mx_workspace_bytes(const nc_mx_matrix* b, int64_t rows, int32_t x_fmt) {
   if (b == nullptr || check_sizes(b->rows, b->cols, b->fmt) != NC_OK || rows < 0 || rows > INT32_MAX) return 0;
-  if (x_fmt < 0 || rows <= kFusedRows) return 0;
-  return check_sizes(rows, b->cols, x_fmt) == NC_OK ? round256(bytes_of(rows, b->cols, x_fmt)) : 0;
+  const size_t part = most_part_bytes(rows, b->rows, chunks_of(b->cols));
+  if (x_fmt < 0 || rows <= kFusedRows) return part;
+  return check_sizes(rows, b->cols, x_fmt) == NC_OK ? part + round256(bytes_of(rows, b->cols, x_fmt)) : 0;
 }
 
 nc_status nc_mx_matmul(const nc_mx_matrix* a, const nc_mx_matrix* b, const nc_mx_out* out, void* ws, size_t ws_bytes,
@@ -129,7 +166,8 @@ nc_status nc_mx_matmul(const nc_mx_matrix* a, const nc_mx_matrix* b, const nc_mx
   p.a = matrix_of(a);
   p.b = matrix_of(b);
   set_out(p, out);
-  return product(p, a->fmt, b->fmt, (hipStream_t)stream);
+  if (ws_bytes > 0 && (ws == nullptr || !aligned16(ws))) return NC_E_WORKSPACE;
+  return product(p, a->fmt, b->fmt, ws, ws_bytes, (hipStream_t)stream);
 }
 
 nc_status nc_mx_linear(const nc_plane* x, int64_t rows, nc_dtype x_dtype, nc_fmt x_fmt, nc_mx_rule rule,
@@ -140,6 +178,7 @@ nc_status nc_mx_linear(const nc_plane* x, int64_t rows, nc_dtype x_dtype, nc_fmt
   if ((s = check_out(out, rows, w->rows)) != NC_OK) return s;
   if (rows == 0 || w->rows == 0) return NC_OK;
   if (w->cols > 0 && (s = check_plane(x, x_dtype, 0)) != NC_OK) return s;
+  if (ws_bytes > 0 && (ws == nullptr || !aligned16(ws))) return NC_E_WORKSPACE;
   MxProduct p = {};
   p.b = matrix_of(w);
   set_out(p, out);
@@ -149,16 +188,16 @@ nc_status nc_mx_linear(const nc_plane* x, int64_t rows, nc_dtype x_dtype, nc_fmt
     p.x_stride = w->cols > 0 ? x->stride : 0;
     p.x_dtype = x_dtype;
     p.rule = rule;
-    return product(p, x_fmt, w->fmt, (hipStream_t)stream);
+    return product(p, x_fmt, w->fmt, ws, ws_bytes, (hipStream_t)stream);
   }
-  const size_t need = nc_mx_workspace_bytes(w, rows, x_fmt);
-  if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return NC_E_WORKSPACE;
+  const size_t need = round256(bytes_of(rows, w->cols, x_fmt));
+  if (ws_bytes < need) return NC_E_WORKSPACE;
   p.a = matrix_of((uint8_t*)ws, rows, w->cols, x_fmt);
   if (w->cols > 0) {
     const hipError_t e = launch_mx_write(&p.a, nullptr, x_fmt, input(x), x_dtype, rule, (hipStream_t)stream);
     if (e != hipSuccess) return hip_status(e);
   }
-  return product(p, x_fmt, w->fmt, (hipStream_t)stream);
+  return product(p, x_fmt, w->fmt, (uint8_t*)ws + need, ws_bytes - need, (hipStream_t)stream);
 }
 
 nc_status nc_act_forward(nc_act act, int64_t rows, int64_t cols, const nc_plane* gate, const nc_plane* up,

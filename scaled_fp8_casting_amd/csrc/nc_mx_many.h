@@ -1,0 +1,305 @@
+// Products with many rows: the matrix units bound them.
+//
+// Four waves, two by two, each with W x W tiles of 32 x 32 results in registers
+// (W = 4: a workgroup has 256 x 256 results and a compute unit for itself; W = 2:
+// 128 x 128, two workgroups a compute unit).  Every operand byte of a stage -- two
+// steps of 64 columns of two E2M1 operands, one step where one has 8 bits -- goes
+// from memory to LDS once for the workgroup and from LDS to registers once for each
+// wave that multiplies it; W = 4 reads 64 bytes of LDS for 8 matrix instructions.
+//
+// The copies into LDS are asynchronous and take no registers.  kStages of them are
+// in flight in a ring of LDS slots:
+//
+//   stage s:  wait until the copies of stage s + 1 have landed (all waves: barrier)
+//             read stage s + 1 from LDS into the other set of registers
+//             start the copies of stage s + kStages into the slot of stage s, which
+//               all waves had read before the barrier
+//             multiply stage s
+//
+// so the multiplications run beside the reads for the next stage, and a copy has
+// kStages - 1 stages to arrive.  Layout in LDS is that in memory, the instruction's
+// order: a wave's reads are runs of 1 KiB and meet no bank twice.  Scales go the
+// same way, a dword a lane and chunk, a chunk ahead of their codes.
+#pragma once
+
+#include <type_traits>
+
+#include "nc_mx_mul.h"
+
+namespace nc {
+
+constexpr int kMxStages = 4;       // stages in flight, and slots of the ring
+constexpr int kMxScaleSlots = 4;   // chunks of scales: those of the stages in flight and one ahead
+
+// A copy of 1 KiB from memory to LDS, 16 bytes a lane from base + off; at: byte of
+// LDS of the first lane's.  Written as assembly because the compiler waits for all
+// copies in flight before any read of LDS; waiting is the caller's.  It has no
+// result that a register would have to be kept for.  M0 holds the LDS address (the
+// compiler never leaves a value in it, and nothing else here uses it), and
+// its write needs a wait state before the use.
+template <int UNITS> __device__ __forceinline__ void mx_copy(const uint8_t* base, uint32_t off, uint32_t at) {
+  if constexpr (UNITS == 2)
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
+                     ::"s"(at), "v"(off), "s"(base) : "memory");
+  else
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+}
+// 256 bytes, a dword a lane.
+__device__ __forceinline__ void mx_copy_scales(const uint8_t* base, uint32_t off, uint32_t at) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+}
+template <int N> __device__ __forceinline__ void mx_wait() { __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void mx_barrier() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+}
+
+template <int FA, int FB, int W> struct MxTile {
+  static constexpr int STEPS = FA == NC_E2M1 && FB == NC_E2M1 ? 2 : 1;     // of a stage
+  static constexpr int SPC = 4 / STEPS;                                    // stages of a chunk
+  static constexpr int STRIPS = 2 * W;                                     // of either operand, of the workgroup
+  static constexpr int UA = STEPS * mx_step_bytes(FA) / 1024, UB = STEPS * mx_step_bytes(FB) / 1024;   // KiB of a strip and stage
+  static constexpr int STAGE = STRIPS * (UA + UB) * 1024;
+  static constexpr int SCALES = 2 * STRIPS * kMxScaleBytes;                // of a chunk
+  static constexpr int LDS = kMxStages * STAGE + kMxScaleSlots * SCALES;
+  static constexpr int OWN = STRIPS / 2;                                   // strips of either operand whose copies a wave makes ... of a pair of waves
+  static constexpr int COPIES_SC = (W + SPC - 1) / SPC;                    // copies of scales of a wave and stage
+  static constexpr int COPIES = W / 2 * (UA + UB) + COPIES_SC;             // copies of a wave and stage
+  static constexpr int EPI = 4 * 32 * (32 * W + 4) * 4;                    // results on their way out
+  static_assert(EPI <= LDS, "results fit where the operands were");
+};
+
+template <int FA, int FB, bool WIDE, int W>
+__global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
+  using T = MxTile<FA, FB, W>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+
+  // Workgroups follow each other over the eight XCDs: each XCD gets a run of
+  // neighbouring tiles, in columns of four, whose operands its L2 holds.
+  const uint32_t tiles_a = ((uint32_t)p.a.strips + T::STRIPS - 1) / T::STRIPS, tiles_b = ((uint32_t)p.b.strips + T::STRIPS - 1) / T::STRIPS;
+  const uint32_t tiles = tiles_a * tiles_b;
+  uint32_t tile = blockIdx.x % tiles;
+  const uint32_t split = blockIdx.x / tiles;
+  {
+    const uint32_t each = tiles / 8, more = tiles % 8, xcd = tile % 8, i = tile / 8;
+    tile = xcd * each + min(xcd, more) + i;
+  }
+  uint32_t ta, tb;
+  {
+    const uint32_t band = tile / (4 * tiles_b), first = band * 4, high = min(4u, tiles_a - first), in = tile - band * 4 * tiles_b;
+    ta = first + in % high;
+    tb = in / high;
+  }
+  const int32_t strip_a = (int32_t)ta * T::STRIPS, strip_b = (int32_t)tb * T::STRIPS;
+
+  // this split's chunks
+  const int32_t chunks = p.b.chunks;
+  const int32_t c0 = (int32_t)((int64_t)chunks * split / p.splits), c1 = (int32_t)((int64_t)chunks * (split + 1) / p.splits);
+  const int32_t stages = (c1 - c0) * T::SPC;
+
+  // what this wave copies: W / 2 strips of a and of b, and their scales; strips
+  // past the end are the last one's again
+  const uint8_t *ga[W / 2], *gb[W / 2], *gs[W];
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) {
+    const int64_t sa = min(strip_a + wave * (W / 2) + i, p.a.strips - 1), sb = min(strip_b + wave * (W / 2) + i, p.b.strips - 1);
+    ga[i] = p.a.codes + (sa * chunks + c0) * mx_chunk_bytes(FA);
+    gb[i] = p.b.codes + (sb * chunks + c0) * mx_chunk_bytes(FB);
+    gs[i] = p.a.scales + (sa * chunks + c0) * kMxScaleBytes;
+    gs[W / 2 + i] = p.b.scales + (sb * chunks + c0) * kMxScaleBytes;
+  }
+  const uint32_t off16 = (uint32_t)lane * 16, off4 = (uint32_t)lane * 4;
+  const uint32_t sc0 = lds0 + kMxStages * T::STAGE;
+  // place of the wave's i-th strip's scales in a slot: a's strips, then b's
+  const auto scale_at = [&](int i) { return (uint32_t)((i < W / 2 ? wave * (W / 2) + i : T::STRIPS + wave * (W / 2) + i - W / 2) * kMxScaleBytes); };
+
+  const auto copy_stage = [&](int32_t t) {
+    const uint32_t at = lds0 + (uint32_t)(t % kMxStages) * T::STAGE;
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      mx_copy<T::UA>(ga[i] + (int64_t)t * (T::UA * 1024), off16, at + (uint32_t)(wave * (W / 2) + i) * (T::UA * 1024));
+      mx_copy<T::UB>(gb[i] + (int64_t)t * (T::UB * 1024), off16, at + T::STRIPS * T::UA * 1024 + (uint32_t)(wave * (W / 2) + i) * (T::UB * 1024));
+    }
+  };
+  // with stage t go scales of the chunk after its own
+  const auto copy_scales = [&](int32_t t) {
+    const int32_t c = min(t / T::SPC + 1, c1 - c0 - 1);
+#pragma unroll
+    for (int i = 0; i < T::COPIES_SC; ++i) {
+      const int j = (t % T::SPC * T::COPIES_SC + i) % W;
+      mx_copy_scales(gs[j] + (int64_t)c * kMxScaleBytes, off4, sc0 + (uint32_t)((t / T::SPC + 1) % kMxScaleSlots) * T::SCALES + scale_at(j));
+    }
+  };
+
+  f32x16_t acc[W][W];
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+  if (stages > 0) {
+    const int wa = wave >> 1, wb = wave & 1;   // this wave's quarter of the results
+    struct Set { MxFrag<FA> a[W][T::STEPS]; MxFrag<FB> b[W][T::STEPS]; } set[2];
+    uint32_t xa[W], xb[W], na[W], nb[W];
+    const auto read_stage = [&](int32_t t, Set& f) {
+      const uint8_t* at = lds + (t % kMxStages) * T::STAGE;
+#pragma unroll
+      for (int s = 0; s < T::STEPS; ++s)
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          f.a[i][s] = mx_frag<FA>(at + (wa * W + i) * (T::UA * 1024) + s * mx_step_bytes(FA), lane);
+          f.b[i][s] = mx_frag<FB>(at + T::STRIPS * T::UA * 1024 + (wb * W + i) * (T::UB * 1024) + s * mx_step_bytes(FB), lane);
+        }
+    };
+    const auto read_scales = [&](int32_t c, uint32_t (&a)[W], uint32_t (&b)[W]) {
+      const uint8_t* at = lds + kMxStages * T::STAGE + (c % kMxScaleSlots) * T::SCALES + lane * 4;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        a[i] = *reinterpret_cast<const uint32_t*>(at + (wa * W + i) * kMxScaleBytes);
+        b[i] = *reinterpret_cast<const uint32_t*>(at + (T::STRIPS + wb * W + i) * kMxScaleBytes);
+      }
+    };
+
+    const auto multiply = [&](const Set& f, int s, int byte) {
+      if constexpr (WIDE) {
+        MxWide b[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const MxScales x = mx_scales<true>(xb[j], lane);
+          b[j] = mx_widen<FB>(f.b[j][s], (x.block0 >> (8 * byte)) & 255u, (x.block1 >> (8 * byte)) & 255u);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const MxScales x = mx_scales<true>(xa[i], lane);
+          const MxWide a = mx_widen<FA>(f.a[i][s], (x.block0 >> (8 * byte)) & 255u, (x.block1 >> (8 * byte)) & 255u);
+#pragma unroll
+          for (int j = 0; j < W; ++j) acc[i][j] = mx_mma_wide(a, b[j], acc[i][j]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            if (byte == 0) acc[i][j] = mx_mma<FA, FB, 0>(f.a[i][s], f.b[j][s], acc[i][j], xa[i], xb[j]);
+            else if (byte == 1) acc[i][j] = mx_mma<FA, FB, 1>(f.a[i][s], f.b[j][s], acc[i][j], xa[i], xb[j]);
+            else if (byte == 2) acc[i][j] = mx_mma<FA, FB, 2>(f.a[i][s], f.b[j][s], acc[i][j], xa[i], xb[j]);
+            else acc[i][j] = mx_mma<FA, FB, 3>(f.a[i][s], f.b[j][s], acc[i][j], xa[i], xb[j]);
+          }
+      }
+    };
+    // One chunk.  FROM: -1 where copies go on; else how many stages have gone by
+    // since the last copy was started, so that the waits know what is in flight.
+    const auto chunk = [&](int32_t c, auto from) {
+      constexpr int FROM = decltype(from)::value;
+#pragma unroll
+      for (int u = 0; u < T::SPC; ++u) {
+        const int32_t t = c * T::SPC + u;
+        Set &now = set[u & 1], &next = set[(u & 1) ^ 1];
+        constexpr int N = T::COPIES;
+        const int gone = FROM < 0 ? 0 : FROM + u;
+        if (gone == 0) mx_wait<(kMxStages - 2) * N>();
+        else if (gone == 1) mx_wait<(kMxStages - 3) * N>();
+        else mx_wait<0>();
+        mx_barrier();
+        if (gone < kMxStages - 1) {
+          read_stage(t + 1, next);
+          if (u == T::SPC - 1) read_scales(c + 1, na, nb);
+        }
+        if (FROM < 0) {
+          copy_stage(t + kMxStages);
+          copy_scales(t + kMxStages);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < T::STEPS; ++s) multiply(now, s, u * T::STEPS + s);
+        __builtin_amdgcn_sched_barrier(0);
+        if (u == T::SPC - 1) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            xa[i] = na[i];
+            xb[i] = nb[i];
+          }
+        }
+      }
+    };
+
+    // the first chunk's scales, then the ring
+#pragma unroll
+    for (int j = 0; j < W; ++j) mx_copy_scales(gs[j], off4, sc0 + scale_at(j));
+#pragma unroll
+    for (int t = 0; t < kMxStages; ++t)
+      if (t < stages) {
+        copy_stage(t);
+        copy_scales(t);
+      }
+    mx_wait<0>();
+    mx_barrier();
+    read_stage(0, set[0]);
+    read_scales(0, xa, xb);
+    static_assert(kMxStages == 4, "the last four stages: one chunk or two");
+    const int32_t all = c1 - c0;
+    int32_t c = 0;
+    for (; c < all - 4 / T::SPC; ++c) chunk(c, std::integral_constant<int, -1>{});
+    if (T::SPC == 4 || all > 1) chunk(c++, std::integral_constant<int, 0>{});
+    if (T::SPC == 2) chunk(c, std::integral_constant<int, 2>{});
+  }
+
+  // Results through LDS, a wave's 32 rows at a time, so that a row goes out in one
+  // run.  Each wave has a place of its own.
+  mx_wait<0>();
+  mx_barrier();
+  constexpr int COLS = 32 * W;
+  float (*hold)[COLS + 4] = reinterpret_cast<float (*)[COLS + 4]>(lds + wave * (T::EPI / 4));
+  const int64_t row0 = ((int64_t)strip_a + (wave >> 1) * W) * kMxRows, col0 = ((int64_t)strip_b + (wave & 1) * W) * kMxRows;
+  MxProduct o = p;
+  if (p.splits > 1) {
+    o.out = p.part + (int64_t)split * p.a.rows * p.b.rows;
+    o.out_stride = p.b.rows;
+    o.out_dtype = NC_F32;
+    o.bias = nullptr;
+    o.accumulate = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) hold[8 * (e / 4) + 4 * (lane >> 5) + e % 4][32 * j + (lane & 31)] = acc[i][j][e];
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 4
+    for (int r = lane / (COLS / 4); r < 32; r += 64 / (COLS / 4)) {
+      const int c = lane % (COLS / 4) * 4;
+      const int64_t row = row0 + 32 * i + r, col = col0 + c;
+      if (row < p.a.rows && col < p.b.rows) {
+        const float y[4] = {hold[r][c], hold[r][c + 1], hold[r][c + 2], hold[r][c + 3]};
+        mx_store4(o, row, col, p.b.rows - col, y);
+      }
+    }
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
+template <int FA, int FB, bool WIDE, int W> hipError_t mx_many_run(const MxProduct& p, hipStream_t stream) {
+  constexpr int S = 2 * W;
+  const uint32_t tiles = ((uint32_t)p.a.strips + S - 1) / S * (((uint32_t)p.b.strips + S - 1) / S);
+  mx_many<FA, FB, WIDE, W><<<dim3(tiles * (uint32_t)p.splits), dim3(256), 0, stream>>>(p);
+  return hipGetLastError();
+}
+template <int FA, int FB> hipError_t mx_many_launch(const MxProduct& p, int w, hipStream_t stream) {
+  if constexpr (FA != NC_E2M1 || FB != NC_E2M1) {
+    // four times the operands' registers: no room for W = 4
+    if (p.out_dtype == NC_F32) return mx_many_run<FA, FB, true, 2>(p, stream);
+  }
+  return w == 4 ? mx_many_run<FA, FB, false, 4>(p, stream) : mx_many_run<FA, FB, false, 2>(p, stream);
+}
+
+hipError_t mx_many_e2m1(const MxProduct& p, int fb, int w, hipStream_t stream);
+hipError_t mx_many_e4m3(const MxProduct& p, int fb, int w, hipStream_t stream);
+hipError_t mx_many_e5m2(const MxProduct& p, int fb, int w, hipStream_t stream);
+
+}  // namespace nc
