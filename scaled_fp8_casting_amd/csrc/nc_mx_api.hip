@@ -53,9 +53,6 @@ size_t bytes_of(int64_t rows, int64_t cols, int32_t fmt) {
   return (size_t)(strips_of(rows) * chunks_of(cols)) * (size_t)(mx_chunk_bytes(fmt) + kMxScaleBytes);
 }
 
-// Rows of a linear layer that the product quantises itself.
-constexpr int64_t kFusedRows = kMxRows;
-
 nc_status check_out(const nc_mx_out* o, int64_t rows, int64_t cols) {
   if (o == nullptr) return NC_E_ARG;
   if (!valid_dtype(o->dtype)) return NC_E_UNSUPPORTED;
@@ -151,7 +148,7 @@ nc_status nc_mx_read(const nc_mx_matrix* m, const nc_plane* y, nc_dtype dtype, v
 size_t nc_mx_workspace_bytes(const nc_mx_matrix* b, int64_t rows, int32_t x_fmt) {
   if (b == nullptr || check_sizes(b->rows, b->cols, b->fmt) != NC_OK || rows < 0 || rows > INT32_MAX) return 0;
   const size_t part = most_part_bytes(rows, b->rows, chunks_of(b->cols));
-  if (x_fmt < 0 || rows <= kFusedRows) return part;
+  if (x_fmt < 0 || rows <= kMxFusedRows) return part;
   return check_sizes(rows, b->cols, x_fmt) == NC_OK ? part + round256(bytes_of(rows, b->cols, x_fmt)) : 0;
 }
 
@@ -182,7 +179,7 @@ nc_status nc_mx_linear(const nc_plane* x, int64_t rows, nc_dtype x_dtype, nc_fmt
   MxProduct p = {};
   p.b = matrix_of(w);
   set_out(p, out);
-  if (rows <= kFusedRows) {
+  if (rows <= kMxFusedRows) {
     p.a = matrix_of(nullptr, rows, w->cols, x_fmt);
     p.x = w->cols > 0 ? x->data : nullptr;
     p.x_stride = w->cols > 0 ? x->stride : 0;

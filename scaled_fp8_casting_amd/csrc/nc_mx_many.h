@@ -10,14 +10,16 @@
 // The copies into LDS are asynchronous and take no registers.  kStages of them are
 // in flight in a ring of LDS slots:
 //
-//   stage s:  wait until the copies of stage s + 1 have landed (all waves: barrier)
-//             read stage s + 1 from LDS into the other set of registers
-//             start the copies of stage s + kStages into the slot of stage s, which
-//               all waves had read before the barrier
-//             multiply stage s
+//   stage s:  start multiplying stage s, whose operands are in registers
+//             wait until the copies of stage s + 1 have landed (all waves: barrier)
+//             between the other products, one by one: read stage s + 1 from LDS into
+//               the other set of registers, and start the copies of stage s + kStages
+//               into the slot of stage s, which all waves had read before the barrier
 //
-// so the multiplications run beside the reads for the next stage, and a copy has
-// kStages - 1 stages to arrive.  Layout in LDS is that in memory, the instruction's
+// so the matrix units have work at the barrier and beside the reads, and a copy has
+// kStages - 1 stages to arrive.  Issued in one go, the copies and reads of a stage
+// held the products up for as long as memory took to accept them (8192^3 E4M3: 543
+// us, the matrix units busy for 49% of it).  Layout in LDS is that in memory, the instruction's
 // order: a wave's reads are runs of 1 KiB and meet no bank twice.  Scales go the
 // same way, a dword a lane and chunk, a chunk ahead of their codes.
 #pragma once
@@ -37,12 +39,8 @@ constexpr int kMxScaleSlots = 4;   // chunks of scales: those of the stages in f
 // result that a register would have to be kept for.  M0 holds the LDS address (the
 // compiler never leaves a value in it, and nothing else here uses it), and
 // its write needs a wait state before the use.
-template <int UNITS> __device__ __forceinline__ void mx_copy(const uint8_t* base, uint32_t off, uint32_t at) {
-  if constexpr (UNITS == 2)
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
-                     ::"s"(at), "v"(off), "s"(base) : "memory");
-  else
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+__device__ __forceinline__ void mx_copy(const uint8_t* base, uint32_t off, uint32_t at) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
 }
 // 256 bytes, a dword a lane.
 __device__ __forceinline__ void mx_copy_scales(const uint8_t* base, uint32_t off, uint32_t at) {
@@ -63,7 +61,6 @@ template <int FA, int FB, int W> struct MxTile {
   static constexpr int STAGE = STRIPS * (UA + UB) * 1024;
   static constexpr int SCALES = 2 * STRIPS * kMxScaleBytes;                // of a chunk
   static constexpr int LDS = kMxStages * STAGE + kMxScaleSlots * SCALES;
-  static constexpr int OWN = STRIPS / 2;                                   // strips of either operand whose copies a wave makes ... of a pair of waves
   static constexpr int COPIES_SC = (W + SPC - 1) / SPC;                    // copies of scales of a wave and stage
   static constexpr int COPIES = W / 2 * (UA + UB) + COPIES_SC;             // copies of a wave and stage
   static constexpr int EPI = 4 * 32 * (32 * W + 4) * 4;                    // results on their way out
@@ -116,20 +113,21 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
   // place of the wave's i-th strip's scales in a slot: a's strips, then b's
   const auto scale_at = [&](int i) { return (uint32_t)((i < W / 2 ? wave * (W / 2) + i : T::STRIPS + wave * (W / 2) + i - W / 2) * kMxScaleBytes); };
 
-  const auto copy_stage = [&](int32_t t) {
+  // the i-th of this wave's copies of stage t: its strips of a, of b, scales
+  constexpr int CA = W / 2 * T::UA, CB = W / 2 * T::UB;
+  const auto copy = [&](int32_t t, int i) {
     const uint32_t at = lds0 + (uint32_t)(t % kMxStages) * T::STAGE;
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      mx_copy<T::UA>(ga[i] + (int64_t)t * (T::UA * 1024), off16, at + (uint32_t)(wave * (W / 2) + i) * (T::UA * 1024));
-      mx_copy<T::UB>(gb[i] + (int64_t)t * (T::UB * 1024), off16, at + T::STRIPS * T::UA * 1024 + (uint32_t)(wave * (W / 2) + i) * (T::UB * 1024));
-    }
-  };
-  // with stage t go scales of the chunk after its own
-  const auto copy_scales = [&](int32_t t) {
-    const int32_t c = min(t / T::SPC + 1, c1 - c0 - 1);
-#pragma unroll
-    for (int i = 0; i < T::COPIES_SC; ++i) {
-      const int j = (t % T::SPC * T::COPIES_SC + i) % W;
+    if (i < CA) {
+      const int j = i / T::UA, u = i % T::UA;
+      mx_copy(ga[j] + (int64_t)t * (T::UA * 1024) + u * 1024, off16, at + (uint32_t)(wave * (W / 2) + j) * (T::UA * 1024) + u * 1024);
+    } else if (i < CA + CB) {
+      const int j = (i - CA) / T::UB, u = (i - CA) % T::UB;
+      mx_copy(gb[j] + (int64_t)t * (T::UB * 1024) + u * 1024, off16,
+              at + T::STRIPS * T::UA * 1024 + (uint32_t)(wave * (W / 2) + j) * (T::UB * 1024) + u * 1024);
+    } else {
+      // with stage t go scales of the chunk after its own
+      const int32_t c = min(t / T::SPC + 1, c1 - c0 - 1);
+      const int j = (t % T::SPC * T::COPIES_SC + i - CA - CB) % W;
       mx_copy_scales(gs[j] + (int64_t)c * kMxScaleBytes, off4, sc0 + (uint32_t)((t / T::SPC + 1) % kMxScaleSlots) * T::SCALES + scale_at(j));
     }
   };
@@ -144,17 +142,26 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
 
   if (stages > 0) {
     const int wa = wave >> 1, wb = wave & 1;   // this wave's quarter of the results
-    struct Set { MxFrag<FA> a[W][T::STEPS]; MxFrag<FB> b[W][T::STEPS]; } set[2];
+    struct Set { u32x4 a[W][T::UA], b[W][T::UB]; } set[2];
     uint32_t xa[W], xb[W], na[W], nb[W];
-    const auto read_stage = [&](int32_t t, Set& f) {
-      const uint8_t* at = lds + (t % kMxStages) * T::STAGE;
+    constexpr int READS = W * (T::UA + T::UB);
+    // the i-th read of a stage: in the order in which the products take them
+    const auto read = [&](int32_t t, Set& f, int i) {
+      const uint8_t* at = lds + (t % kMxStages) * T::STAGE + lane * 16;
+      if (i < W * T::UB) f.b[i % W][i / W] = *reinterpret_cast<const u32x4*>(at + T::STRIPS * T::UA * 1024 + (wb * W + i % W) * (T::UB * 1024) + i / W * 1024);
+      else f.a[(i - W * T::UB) % W][(i - W * T::UB) / W] = *reinterpret_cast<const u32x4*>(at + (wa * W + (i - W * T::UB) % W) * (T::UA * 1024) + (i - W * T::UB) / W * 1024);
+    };
+    const auto frag_a = [&](const Set& f, int i, int s) {
+      MxFrag<FA> r;
 #pragma unroll
-      for (int s = 0; s < T::STEPS; ++s)
+      for (int h = 0; h < T::UA / T::STEPS; ++h) r.w[h] = f.a[i][s * (T::UA / T::STEPS) + h];
+      return r;
+    };
+    const auto frag_b = [&](const Set& f, int j, int s) {
+      MxFrag<FB> r;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          f.a[i][s] = mx_frag<FA>(at + (wa * W + i) * (T::UA * 1024) + s * mx_step_bytes(FA), lane);
-          f.b[i][s] = mx_frag<FB>(at + T::STRIPS * T::UA * 1024 + (wb * W + i) * (T::UB * 1024) + s * mx_step_bytes(FB), lane);
-        }
+      for (int h = 0; h < T::UB / T::STEPS; ++h) r.w[h] = f.b[j][s * (T::UB / T::STEPS) + h];
+      return r;
     };
     const auto read_scales = [&](int32_t c, uint32_t (&a)[W], uint32_t (&b)[W]) {
       const uint8_t* at = lds + kMxStages * T::STAGE + (c % kMxScaleSlots) * T::SCALES + lane * 4;
@@ -165,31 +172,40 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
       }
     };
 
-    const auto multiply = [&](const Set& f, int s, int byte) {
-      if constexpr (WIDE) {
-        MxWide b[W];
+    // One stage's products, with `between` called after each (WIDE: each row) of them.
+    const auto multiply = [&](const Set& f, int u, auto between) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const MxScales x = mx_scales<true>(xb[j], lane);
-          b[j] = mx_widen<FB>(f.b[j][s], (x.block0 >> (8 * byte)) & 255u, (x.block1 >> (8 * byte)) & 255u);
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const MxScales x = mx_scales<true>(xa[i], lane);
-          const MxWide a = mx_widen<FA>(f.a[i][s], (x.block0 >> (8 * byte)) & 255u, (x.block1 >> (8 * byte)) & 255u);
-#pragma unroll
-          for (int j = 0; j < W; ++j) acc[i][j] = mx_mma_wide(a, b[j], acc[i][j]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i)
+      for (int s = 0; s < T::STEPS; ++s) {
+        const int byte = u * T::STEPS + s;
+        if constexpr (WIDE) {
+          MxWide b[W];
 #pragma unroll
           for (int j = 0; j < W; ++j) {
-            if (byte == 0) acc[i][j] = mx_mma<FA, FB, 0>(f.a[i][s], f.b[j][s], acc[i][j], xa[i], xb[j]);
-            else if (byte == 1) acc[i][j] = mx_mma<FA, FB, 1>(f.a[i][s], f.b[j][s], acc[i][j], xa[i], xb[j]);
-            else if (byte == 2) acc[i][j] = mx_mma<FA, FB, 2>(f.a[i][s], f.b[j][s], acc[i][j], xa[i], xb[j]);
-            else acc[i][j] = mx_mma<FA, FB, 3>(f.a[i][s], f.b[j][s], acc[i][j], xa[i], xb[j]);
+            const MxScales x = mx_scales<true>(xb[j], lane);
+            b[j] = mx_widen<FB>(frag_b(f, j, s), (x.block0 >> (8 * byte)) & 255u, (x.block1 >> (8 * byte)) & 255u);
           }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const MxScales x = mx_scales<true>(xa[i], lane);
+            const MxWide a = mx_widen<FA>(frag_a(f, i, s), (x.block0 >> (8 * byte)) & 255u, (x.block1 >> (8 * byte)) & 255u);
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[i][j] = mx_mma_wide(a, b[j], acc[i][j]);
+            between(s * W + i, T::STEPS * W);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              const MxFrag<FA> a = frag_a(f, i, s);
+              const MxFrag<FB> b = frag_b(f, j, s);
+              if (byte == 0) acc[i][j] = mx_mma<FA, FB, 0>(a, b, acc[i][j], xa[i], xb[j]);
+              else if (byte == 1) acc[i][j] = mx_mma<FA, FB, 1>(a, b, acc[i][j], xa[i], xb[j]);
+              else if (byte == 2) acc[i][j] = mx_mma<FA, FB, 2>(a, b, acc[i][j], xa[i], xb[j]);
+              else acc[i][j] = mx_mma<FA, FB, 3>(a, b, acc[i][j], xa[i], xb[j]);
+              between((s * W + i) * W + j, T::STEPS * W * W);
+            }
+        }
       }
     };
     // One chunk.  FROM: -1 where copies go on; else how many stages have gone by
@@ -199,25 +215,33 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
 #pragma unroll
       for (int u = 0; u < T::SPC; ++u) {
         const int32_t t = c * T::SPC + u;
-        Set &now = set[u & 1], &next = set[(u & 1) ^ 1];
-        constexpr int N = T::COPIES;
+        const Set& now = set[u & 1];
+        Set& next = set[(u & 1) ^ 1];
         const int gone = FROM < 0 ? 0 : FROM + u;
-        if (gone == 0) mx_wait<(kMxStages - 2) * N>();
-        else if (gone == 1) mx_wait<(kMxStages - 3) * N>();
-        else mx_wait<0>();
-        mx_barrier();
-        if (gone < kMxStages - 1) {
-          read_stage(t + 1, next);
-          if (u == T::SPC - 1) read_scales(c + 1, na, nb);
-        }
-        if (FROM < 0) {
-          copy_stage(t + kMxStages);
-          copy_scales(t + kMxStages);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        multiply(now, u, [&](int k, int of) {
+          const int first = WIDE ? 0 : of / 8;           // the barrier comes after this product
+          if (k == first && gone < kMxStages - 1) {
+            if (gone == 0) mx_wait<(kMxStages - 2) * T::COPIES>();
+            else if (gone == 1) mx_wait<(kMxStages - 3) * T::COPIES>();
+            else mx_wait<0>();
+            mx_barrier();
+            if (u == T::SPC - 1) read_scales(c + 1, na, nb);
+          }
+          if (k >= first) {
+            const int at = k - first, n = of - first;
+            if (gone < kMxStages - 1) {
 #pragma unroll
-        for (int s = 0; s < T::STEPS; ++s) multiply(now, s, u * T::STEPS + s);
-        __builtin_amdgcn_sched_barrier(0);
+              for (int i = 0; i < READS; ++i)
+                if (i * n / READS == at) read(t + 1, next, i);
+            }
+            if (FROM < 0) {
+#pragma unroll
+              for (int i = 0; i < T::COPIES; ++i)
+                if (i * n / T::COPIES == at) copy(t + kMxStages, i);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
         if (u == T::SPC - 1) {
 #pragma unroll
           for (int i = 0; i < W; ++i) {
@@ -234,12 +258,13 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
 #pragma unroll
     for (int t = 0; t < kMxStages; ++t)
       if (t < stages) {
-        copy_stage(t);
-        copy_scales(t);
+#pragma unroll
+        for (int i = 0; i < T::COPIES; ++i) copy(t, i);
       }
     mx_wait<0>();
     mx_barrier();
-    read_stage(0, set[0]);
+#pragma unroll
+    for (int i = 0; i < READS; ++i) read(0, set[0], i);
     read_scales(0, xa, xb);
     static_assert(kMxStages == 4, "the last four stages: one chunk or two");
     const int32_t all = c1 - c0;
