@@ -315,8 +315,10 @@ struct MxProduct {
 hipError_t launch_mx_write(const MxMat* m, const MxMat* t, int fmt, const Plane<const void*>& x, int dtype, int rule,
                            hipStream_t stream);
 hipError_t launch_mx_read(const MxMat& m, int fmt, const Plane<void*>& y, int dtype, hipStream_t stream);
-hipError_t launch_mx_few(const MxProduct& p, int fa, int fb, hipStream_t stream);
-hipError_t launch_mx_many(const MxProduct& p, int fa, int fb, int w, hipStream_t stream);   // tiles of 64 w results a side
+// Few rows: t x t strips a workgroup, t 1 or 2 (unquantised rows: 1).  Many rows, at
+// least one column: 64 w x 64 w results a workgroup, w 2 or 4.
+hipError_t launch_mx_few(const MxProduct& p, int fa, int fb, int t, hipStream_t stream);
+hipError_t launch_mx_many(const MxProduct& p, int fa, int fb, int w, hipStream_t stream);
 
 struct ActForward {
   Plane<const void*> gate, up;   // up.p null: no gate

@@ -1,7 +1,8 @@
-// Products with few rows: one strip of 32 rows of a by one strip of b a
-// workgroup, the chunks of 256 columns dealt to its waves in turn, operands
-// straight from memory, the next chunk's under way while one is multiplied.  The
-// bytes of b bound it.  The waves' sums meet in LDS in the waves' order.
+// Products with few rows, and small ones: T strips of 32 rows of a by T strips of b a
+// workgroup, the chunks of 256 columns dealt to its waves in turn, operands straight
+// from memory.  Their bytes bound it: those of b with few rows, else what the
+// workgroups' operands overlap, which T = 2 halves.  The waves' sums meet in LDS in a
+// fixed order.
 //
 // Up to kMxFusedRows unquantised rows (a linear layer's) are quantised on the way:
 // each wave turns the columns of its own chunk into codes, in a place of its own in
@@ -49,90 +50,139 @@ template <int FMT> struct MxChunk {            // a wave's operand of a chunk
   }
 };
 
-template <int FA, int FB, bool WIDE, int ROWS>
+template <int FA, int FB, bool WIDE, int S>
+__device__ __forceinline__ void mx_few_step(f32x16_t& acc, const MxChunk<FA>& a, const MxChunk<FB>& b, const MxScales& xa, const MxScales& xb) {
+  if constexpr (WIDE)
+    acc = mx_mma_wide(mx_widen<FA>(a.f[S], (xa.block0 >> (8 * S)) & 255u, (xa.block1 >> (8 * S)) & 255u),
+                      mx_widen<FB>(b.f[S], (xb.block0 >> (8 * S)) & 255u, (xb.block1 >> (8 * S)) & 255u), acc);
+  else
+    acc = mx_mma<FA, FB, S>(a.f[S], b.f[S], acc, xa.own, xb.own);
+}
+
+template <int FA, int FB, bool WIDE, int ROWS, int T>
 __global__ void __launch_bounds__(64 * kMxFewWaves) mx_few(MxProduct p) {
   constexpr bool FUSED = ROWS != kMxNoRows;
   constexpr int DT = FUSED ? ROWS : NC_BF16;
-  constexpr int PLACE = mx_chunk_bytes(FA) + kMxScaleBytes, SUMS = 32 * 33 * 4;
-  constexpr int EACH = FUSED && PLACE > SUMS ? PLACE : SUMS;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kMxFewWaves * EACH];
+  constexpr int PLACE = mx_chunk_bytes(FA) + kMxScaleBytes;
+  constexpr int HALF = kMxFewWaves / 2, SIDE = 32 * T, LEAD = SIDE + 1;
+  constexpr int SUMS = HALF * SIDE * LEAD * 4;
+  constexpr int LDS = FUSED && kMxFewWaves * PLACE > SUMS ? kMxFewWaves * PLACE : SUMS;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = (int)(threadIdx.x & 63);
-  const uint32_t strip_b = blockIdx.x % (uint32_t)p.b.strips, strip_a = blockIdx.x / (uint32_t)p.b.strips;
-  uint8_t* place = lds + wave * EACH;
-  f32x16_t acc = {};
+  const uint32_t across = ((uint32_t)p.b.strips + T - 1) / T;
+  const int32_t strip_b = (int32_t)(blockIdx.x % across) * T, strip_a = (int32_t)(blockIdx.x / across) * T;
+  uint8_t* place = lds + wave * PLACE;
+  f32x16_t acc[T][T] = {};
   const int32_t chunks = p.b.chunks;
-  const uint8_t* cb = p.b.codes + (int64_t)strip_b * chunks * mx_chunk_bytes(FB);
-  const uint8_t* sb = p.b.scales + (int64_t)strip_b * chunks * kMxScaleBytes;
-  const uint8_t* ca = p.a.codes + (int64_t)strip_a * chunks * mx_chunk_bytes(FA);
-  const uint8_t* sa = p.a.scales + (int64_t)strip_a * chunks * kMxScaleBytes;
-  MxChunk<FA> a;
-  MxChunk<FB> b;
-  const auto load = [&](int32_t c, MxChunk<FA>& x, MxChunk<FB>& y) {
-    y.load(cb + (int64_t)c * mx_chunk_bytes(FB), sb + (int64_t)c * kMxScaleBytes, lane);
-    if constexpr (!FUSED) x.load(ca + (int64_t)c * mx_chunk_bytes(FA), sa + (int64_t)c * kMxScaleBytes, lane);
+  const uint8_t *ca[T], *sa[T], *cb[T], *sb[T];
+#pragma unroll
+  for (int i = 0; i < T; ++i) {                  // strips past the end are the last one's again
+    const int64_t ia = (int64_t)min(strip_a + i, p.a.strips - 1) * chunks, ib = (int64_t)min(strip_b + i, p.b.strips - 1) * chunks;
+    ca[i] = p.a.codes + ia * mx_chunk_bytes(FA);
+    sa[i] = p.a.scales + ia * kMxScaleBytes;
+    cb[i] = p.b.codes + ib * mx_chunk_bytes(FB);
+    sb[i] = p.b.scales + ib * kMxScaleBytes;
+  }
+  MxChunk<FA> a[T];
+  MxChunk<FB> b[T];
+  const auto load = [&](int32_t c, MxChunk<FA> (&x)[T], MxChunk<FB> (&y)[T]) {
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      y[i].load(cb[i] + (int64_t)c * mx_chunk_bytes(FB), sb[i] + (int64_t)c * kMxScaleBytes, lane);
+      if constexpr (!FUSED) x[i].load(ca[i] + (int64_t)c * mx_chunk_bytes(FA), sa[i] + (int64_t)c * kMxScaleBytes, lane);
+    }
   };
-  if (wave < chunks) load(wave, a, b);
-  for (int32_t c = wave; c < chunks; c += kMxFewWaves) {
-    MxChunk<FA> na;
-    MxChunk<FB> nb;
-    if (c + kMxFewWaves < chunks) load(c + kMxFewWaves, na, nb);
-    if constexpr (FUSED) {
-      mx_quantise<FA, DT>(place, p, (int)p.a.rows, (int64_t)c * kMxChunk, lane);
-      a.load(place, place + mx_chunk_bytes(FA), lane);
-    }
-    const MxScales xa = mx_scales<WIDE>(a.scales, lane), xb = mx_scales<WIDE>(b.scales, lane);
-    if constexpr (WIDE) {
+  const auto multiply = [&](MxChunk<FA> (&x)[T], MxChunk<FB> (&y)[T]) {
+    MxScales xa[T], xb[T];
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        acc = mx_mma_wide(mx_widen<FA>(a.f[s], (xa.block0 >> (8 * s)) & 255u, (xa.block1 >> (8 * s)) & 255u),
-                          mx_widen<FB>(b.f[s], (xb.block0 >> (8 * s)) & 255u, (xb.block1 >> (8 * s)) & 255u), acc);
-    } else {
-      acc = mx_mma<FA, FB, 0>(a.f[0], b.f[0], acc, xa.own, xb.own);
-      acc = mx_mma<FA, FB, 1>(a.f[1], b.f[1], acc, xa.own, xb.own);
-      acc = mx_mma<FA, FB, 2>(a.f[2], b.f[2], acc, xa.own, xb.own);
-      acc = mx_mma<FA, FB, 3>(a.f[3], b.f[3], acc, xa.own, xb.own);
+    for (int i = 0; i < T; ++i) {
+      xa[i] = mx_scales<WIDE>(x[i].scales, lane);
+      xb[i] = mx_scales<WIDE>(y[i].scales, lane);
     }
-    b = nb;
-    if constexpr (!FUSED) a = na;
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        mx_few_step<FA, FB, WIDE, 0>(acc[i][j], x[i], y[j], xa[i], xb[j]);
+        mx_few_step<FA, FB, WIDE, 1>(acc[i][j], x[i], y[j], xa[i], xb[j]);
+        mx_few_step<FA, FB, WIDE, 2>(acc[i][j], x[i], y[j], xa[i], xb[j]);
+        mx_few_step<FA, FB, WIDE, 3>(acc[i][j], x[i], y[j], xa[i], xb[j]);
+      }
+  };
+  if constexpr (T == 1) {                        // the next chunk is under way while one is multiplied
+    if (wave < chunks) load(wave, a, b);
+    for (int32_t c = wave; c < chunks; c += kMxFewWaves) {
+      MxChunk<FA> na[T];
+      MxChunk<FB> nb[T];
+      if (c + kMxFewWaves < chunks) load(c + kMxFewWaves, na, nb);
+      if constexpr (FUSED) {
+        mx_quantise<FA, DT>(place, p, (int)p.a.rows, (int64_t)c * kMxChunk, lane);
+        a[0].load(place, place + mx_chunk_bytes(FA), lane);
+      }
+      multiply(a, b);
+      b[0] = nb[0];
+      if constexpr (!FUSED) a[0] = na[0];
+    }
+  } else {                                       // two waves a SIMD take turns
+    for (int32_t c = wave; c < chunks; c += kMxFewWaves) {
+      load(c, a, b);
+      multiply(a, b);
+    }
   }
+  // The second half of the waves leave their sums, the first half add them to their
+  // own; then these meet.
   if constexpr (FUSED) __syncthreads();          // the sums lie where the rows were
-  float (*sums)[32][33] = reinterpret_cast<float (*)[32][33]>(lds);
+  float (*sums)[SIDE][LEAD] = reinterpret_cast<float (*)[SIDE][LEAD]>(lds);
+  const auto leave = [&](bool add) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
-    if (!FUSED || r < p.a.rows) sums[wave][r][lane & 31] = acc[i];
-  }
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+      for (int j = 0; j < T; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = 32 * i + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+          if (!FUSED || r < p.a.rows) {
+            float& y = sums[wave % HALF][r][32 * j + (lane & 31)];
+            y = add ? y + acc[i][j][e] : acc[i][j][e];
+          }
+        }
+  };
+  if (wave >= HALF) leave(false);
   __syncthreads();
-  if (threadIdx.x < 256) {
-    const int r = (int)(threadIdx.x >> 3), c = (int)(threadIdx.x & 7) * 4;
+  if (wave < HALF) leave(true);
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < SIDE * SIDE / 4; i += 64 * kMxFewWaves) {
+    const int r = i / (SIDE / 4), c = i % (SIDE / 4) * 4;
     const int64_t row = (int64_t)strip_a * kMxRows + r, col = (int64_t)strip_b * kMxRows + c;
     if (row < p.a.rows && col < p.b.rows) {
       float y[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < kMxFewWaves; ++w)
+      for (int w = 0; w < HALF; ++w)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] += sums[w][r][c + i];
-      mx_store4(p, row, col, p.b.rows - col, y);
+        for (int e = 0; e < 4; ++e) y[e] += sums[w][r][c + e];
+      MxStore<4>(p, col)(row, y);
     }
   }
 }
 
-template <int FA, int FB, bool WIDE> hipError_t mx_few_run(const MxProduct& p, hipStream_t stream) {
-  const dim3 grid((uint32_t)p.a.strips * (uint32_t)p.b.strips), block(64 * kMxFewWaves);
-  if (p.x == nullptr) mx_few<FA, FB, WIDE, kMxNoRows><<<grid, block, 0, stream>>>(p);
-  else if (p.x_dtype == NC_BF16) mx_few<FA, FB, WIDE, NC_BF16><<<grid, block, 0, stream>>>(p);
-  else mx_few<FA, FB, WIDE, NC_F32><<<grid, block, 0, stream>>>(p);
+template <int FA, int FB, bool WIDE> hipError_t mx_few_run(const MxProduct& p, int t, hipStream_t stream) {
+  const dim3 block(64 * kMxFewWaves);
+  const dim3 grid(((uint32_t)p.a.strips + t - 1) / t * (((uint32_t)p.b.strips + t - 1) / t));
+  if (t == 2) mx_few<FA, FB, WIDE, kMxNoRows, 2><<<grid, block, 0, stream>>>(p);
+  else if (p.x == nullptr) mx_few<FA, FB, WIDE, kMxNoRows, 1><<<grid, block, 0, stream>>>(p);
+  else if (p.x_dtype == NC_BF16) mx_few<FA, FB, WIDE, NC_BF16, 1><<<grid, block, 0, stream>>>(p);
+  else mx_few<FA, FB, WIDE, NC_F32, 1><<<grid, block, 0, stream>>>(p);
   return hipGetLastError();
 }
-template <int FA, int FB> hipError_t mx_few_launch(const MxProduct& p, hipStream_t stream) {
+template <int FA, int FB> hipError_t mx_few_launch(const MxProduct& p, int t, hipStream_t stream) {
   if constexpr (FA != NC_E2M1 || FB != NC_E2M1) {
-    if (p.out_dtype == NC_F32) return mx_few_run<FA, FB, true>(p, stream);
+    if (p.out_dtype == NC_F32) return mx_few_run<FA, FB, true>(p, t, stream);
   }
-  return mx_few_run<FA, FB, false>(p, stream);
+  return mx_few_run<FA, FB, false>(p, t, stream);
 }
 
-hipError_t mx_few_e2m1(const MxProduct& p, int fb, hipStream_t stream);
-hipError_t mx_few_e4m3(const MxProduct& p, int fb, hipStream_t stream);
-hipError_t mx_few_e5m2(const MxProduct& p, int fb, hipStream_t stream);
+hipError_t mx_few_e2m1(const MxProduct& p, int fb, int t, hipStream_t stream);
+hipError_t mx_few_e4m3(const MxProduct& p, int fb, int t, hipStream_t stream);
+hipError_t mx_few_e5m2(const MxProduct& p, int fb, int t, hipStream_t stream);
 
 }  // namespace nc

@@ -7,17 +7,17 @@
 // from memory to LDS once for the workgroup and from LDS to registers once for each
 // wave that multiplies it; W = 4 reads 64 bytes of LDS for 8 matrix instructions.
 //
-// The copies into LDS are asynchronous and take no registers.  kStages of them are
-// in flight in a ring of LDS slots:
+// The copies into LDS are asynchronous and take no registers.  RING stages of them
+// are in flight in as many slots of LDS:
 //
 //   stage s:  start multiplying stage s, whose operands are in registers
 //             wait until the copies of stage s + 1 have landed (all waves: barrier)
 //             between the other products, one by one: read stage s + 1 from LDS into
-//               the other set of registers, and start the copies of stage s + kStages
+//               the other set of registers, and start the copies of stage s + RING
 //               into the slot of stage s, which all waves had read before the barrier
 //
 // so the matrix units have work at the barrier and beside the reads, and a copy has
-// kStages - 1 stages to arrive.  Issued in one go, the copies and reads of a stage
+// RING - 1 stages to arrive (8 slots of W = 2 in place of 4 gained nothing).  Issued in one go, the copies and reads of a stage
 // held the products up for as long as memory took to accept them (8192^3 E4M3: 543
 // us, the matrix units busy for 49% of it).  Layout in LDS is that in memory, the instruction's
 // order: a wave's reads are runs of 1 KiB and meet no bank twice.  Scales go the
@@ -30,21 +30,32 @@
 
 namespace nc {
 
-constexpr int kMxStages = 4;       // stages in flight, and slots of the ring
-constexpr int kMxScaleSlots = 4;   // chunks of scales: those of the stages in flight and one ahead
 
-// A copy of 1 KiB from memory to LDS, 16 bytes a lane from base + off; at: byte of
-// LDS of the first lane's.  Written as assembly because the compiler waits for all
+// A copy of one or two KiB from memory to LDS, 16 bytes a lane from base + off; at:
+// byte of LDS of the first lane's.  Written as assembly because the compiler waits for all
 // copies in flight before any read of LDS; waiting is the caller's.  It has no
 // result that a register would have to be kept for.  M0 holds the LDS address (the
 // compiler never leaves a value in it, and nothing else here uses it), and
 // its write needs a wait state before the use.
-__device__ __forceinline__ void mx_copy(const uint8_t* base, uint32_t off, uint32_t at) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+// Base and place are the wave's (the same in every lane), which the compiler does not
+// always see.
+__device__ __forceinline__ const uint8_t* mx_uniform(const uint8_t* p) {
+  const uint64_t b = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b), hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+  return reinterpret_cast<const uint8_t*>((uintptr_t)((uint64_t)hi << 32 | lo));
+}
+// The instruction's offset counts in memory and in LDS.
+template <int UNITS> __device__ __forceinline__ void mx_copy(const uint8_t* base, uint32_t off, uint32_t at) {
+  const int m0 = __builtin_amdgcn_readfirstlane((int)at);
+  if constexpr (UNITS == 2)
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
+                     ::"s"(m0), "v"(off), "s"(mx_uniform(base)) : "memory");
+  else
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(mx_uniform(base)) : "memory");
 }
 // 256 bytes, a dword a lane.
 __device__ __forceinline__ void mx_copy_scales(const uint8_t* base, uint32_t off, uint32_t at) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(off), "s"(mx_uniform(base)) : "memory");
 }
 template <int N> __device__ __forceinline__ void mx_wait() { __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void mx_barrier() {
@@ -53,6 +64,8 @@ __device__ __forceinline__ void mx_barrier() {
   __asm__ volatile("" ::: "memory");
 }
 
+constexpr int RING = 4;            // stages in flight, and slots
+
 template <int FA, int FB, int W> struct MxTile {
   static constexpr int STEPS = FA == NC_E2M1 && FB == NC_E2M1 ? 2 : 1;     // of a stage
   static constexpr int SPC = 4 / STEPS;                                    // stages of a chunk
@@ -60,10 +73,13 @@ template <int FA, int FB, int W> struct MxTile {
   static constexpr int UA = STEPS * mx_step_bytes(FA) / 1024, UB = STEPS * mx_step_bytes(FB) / 1024;   // KiB of a strip and stage
   static constexpr int STAGE = STRIPS * (UA + UB) * 1024;
   static constexpr int SCALES = 2 * STRIPS * kMxScaleBytes;                // of a chunk
-  static constexpr int LDS = kMxStages * STAGE + kMxScaleSlots * SCALES;
+  static constexpr int SLOTS = 4;                                          // chunks of scales: those of the stages in flight and more ahead
+  static constexpr int LDS = RING * STAGE + SLOTS * SCALES;
   static constexpr int COPIES_SC = (W + SPC - 1) / SPC;                    // copies of scales of a wave and stage
-  static constexpr int COPIES = W / 2 * (UA + UB) + COPIES_SC;             // copies of a wave and stage
-  static constexpr int EPI = 4 * 32 * (32 * W + 4) * 4;                    // results on their way out
+  static constexpr int COPIES = W / 2 * (UA + UB);                         // other copies of a wave and stage
+  static constexpr int ROW_EPI = 4 * 32 * (32 * W + 4) * 4;                // a row of tiles of each wave, on its way out
+  static constexpr int ROWS = W % 2 == 0 && 2 * ROW_EPI <= LDS ? 2 : 1;    // rows of tiles at a time
+  static constexpr int EPI = ROWS * ROW_EPI;
   static_assert(EPI <= LDS, "results fit where the operands were");
 };
 
@@ -97,39 +113,34 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
   const int32_t c0 = (int32_t)((int64_t)chunks * split / p.splits), c1 = (int32_t)((int64_t)chunks * (split + 1) / p.splits);
   const int32_t stages = (c1 - c0) * T::SPC;
 
-  // what this wave copies: W / 2 strips of a and of b, and their scales; strips
-  // past the end are the last one's again
+  // What this wave copies: W / 2 strips of a and of b, and their scales; strips
+  // past the end are the last one's again.  The pointers go on with every copy.
   const uint8_t *ga[W / 2], *gb[W / 2], *gs[W];
 #pragma unroll
   for (int i = 0; i < W / 2; ++i) {
-    const int64_t sa = min(strip_a + wave * (W / 2) + i, p.a.strips - 1), sb = min(strip_b + wave * (W / 2) + i, p.b.strips - 1);
-    ga[i] = p.a.codes + (sa * chunks + c0) * mx_chunk_bytes(FA);
-    gb[i] = p.b.codes + (sb * chunks + c0) * mx_chunk_bytes(FB);
-    gs[i] = p.a.scales + (sa * chunks + c0) * kMxScaleBytes;
-    gs[W / 2 + i] = p.b.scales + (sb * chunks + c0) * kMxScaleBytes;
+    const int64_t sa = (int64_t)min(strip_a + wave * (W / 2) + i, p.a.strips - 1) * chunks + c0;
+    const int64_t sb = (int64_t)min(strip_b + wave * (W / 2) + i, p.b.strips - 1) * chunks + c0;
+    ga[i] = p.a.codes + sa * mx_chunk_bytes(FA);
+    gb[i] = p.b.codes + sb * mx_chunk_bytes(FB);
+    gs[i] = p.a.scales + sa * kMxScaleBytes;
+    gs[W / 2 + i] = p.b.scales + sb * kMxScaleBytes;
   }
   const uint32_t off16 = (uint32_t)lane * 16, off4 = (uint32_t)lane * 4;
-  const uint32_t sc0 = lds0 + kMxStages * T::STAGE;
-  // place of the wave's i-th strip's scales in a slot: a's strips, then b's
-  const auto scale_at = [&](int i) { return (uint32_t)((i < W / 2 ? wave * (W / 2) + i : T::STRIPS + wave * (W / 2) + i - W / 2) * kMxScaleBytes); };
-
-  // the i-th of this wave's copies of stage t: its strips of a, of b, scales
-  constexpr int CA = W / 2 * T::UA, CB = W / 2 * T::UB;
-  const auto copy = [&](int32_t t, int i) {
-    const uint32_t at = lds0 + (uint32_t)(t % kMxStages) * T::STAGE;
-    if (i < CA) {
-      const int j = i / T::UA, u = i % T::UA;
-      mx_copy(ga[j] + (int64_t)t * (T::UA * 1024) + u * 1024, off16, at + (uint32_t)(wave * (W / 2) + j) * (T::UA * 1024) + u * 1024);
-    } else if (i < CA + CB) {
-      const int j = (i - CA) / T::UB, u = (i - CA) % T::UB;
-      mx_copy(gb[j] + (int64_t)t * (T::UB * 1024) + u * 1024, off16,
-              at + T::STRIPS * T::UA * 1024 + (uint32_t)(wave * (W / 2) + j) * (T::UB * 1024) + u * 1024);
+  const uint32_t codes0 = lds0 + (uint32_t)wave * (W / 2) * (T::UA * 1024), sc0 = lds0 + RING * T::STAGE + (uint32_t)wave * (W / 2) * kMxScaleBytes;
+  // the i-th of this wave's strips, of a, then of b, in the slot at `slot`
+  const auto copy = [&](uint32_t slot, int i) {
+    if (i < W / 2) {
+      mx_copy<T::UA>(ga[i], off16, codes0 + slot + i * (T::UA * 1024));
+      ga[i] += T::UA * 1024;
     } else {
-      // with stage t go scales of the chunk after its own
-      const int32_t c = min(t / T::SPC + 1, c1 - c0 - 1);
-      const int j = (t % T::SPC * T::COPIES_SC + i - CA - CB) % W;
-      mx_copy_scales(gs[j] + (int64_t)c * kMxScaleBytes, off4, sc0 + (uint32_t)((t / T::SPC + 1) % kMxScaleSlots) * T::SCALES + scale_at(j));
+      mx_copy<T::UB>(gb[i - W / 2], off16, codes0 + slot + T::STRIPS * T::UA * 1024 + (i - W / 2) * (T::UB * 1024) + (uint32_t)wave * (W / 2) * ((T::UB - T::UA) * 1024));
+      gb[i - W / 2] += T::UB * 1024;
     }
+  };
+  // the scales of a chunk for the wave's j-th strip
+  const auto copy_scales = [&](int32_t c, int j) {
+    mx_copy_scales(gs[j] + (int64_t)min(c, c1 - c0 - 1) * kMxScaleBytes, off4,
+                   sc0 + (uint32_t)(c % T::SLOTS) * T::SCALES + (uint32_t)(j < W / 2 ? j : T::STRIPS + j - W / 2) * kMxScaleBytes);
   };
 
   f32x16_t acc[W][W];
@@ -140,14 +151,14 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  if (stages > 0) {
+  {
     const int wa = wave >> 1, wb = wave & 1;   // this wave's quarter of the results
     struct Set { u32x4 a[W][T::UA], b[W][T::UB]; } set[2];
     uint32_t xa[W], xb[W], na[W], nb[W];
     constexpr int READS = W * (T::UA + T::UB);
     // the i-th read of a stage: in the order in which the products take them
     const auto read = [&](int32_t t, Set& f, int i) {
-      const uint8_t* at = lds + (t % kMxStages) * T::STAGE + lane * 16;
+      const uint8_t* at = lds + (t % RING) * T::STAGE + lane * 16;
       if (i < W * T::UB) f.b[i % W][i / W] = *reinterpret_cast<const u32x4*>(at + T::STRIPS * T::UA * 1024 + (wb * W + i % W) * (T::UB * 1024) + i / W * 1024);
       else f.a[(i - W * T::UB) % W][(i - W * T::UB) / W] = *reinterpret_cast<const u32x4*>(at + (wa * W + (i - W * T::UB) % W) * (T::UA * 1024) + (i - W * T::UB) / W * 1024);
     };
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
       return r;
     };
     const auto read_scales = [&](int32_t c, uint32_t (&a)[W], uint32_t (&b)[W]) {
-      const uint8_t* at = lds + kMxStages * T::STAGE + (c % kMxScaleSlots) * T::SCALES + lane * 4;
+      const uint8_t* at = lds + RING * T::STAGE + (c % T::SLOTS) * T::SCALES + lane * 4;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         a[i] = *reinterpret_cast<const uint32_t*>(at + (wa * W + i) * kMxScaleBytes);
@@ -208,36 +219,36 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
         }
       }
     };
-    // One chunk.  FROM: -1 where copies go on; else how many stages have gone by
-    // since the last copy was started, so that the waits know what is in flight.
-    const auto chunk = [&](int32_t c, auto from) {
-      constexpr int FROM = decltype(from)::value;
+    // One chunk.  Once no copies are left to start, the first wait is for all that
+    // are in flight; the last stage then reads one that is not there, for nobody.
+    const auto chunk = [&](int32_t c, auto more) {
+      constexpr bool MORE = decltype(more)::value;
 #pragma unroll
       for (int u = 0; u < T::SPC; ++u) {
         const int32_t t = c * T::SPC + u;
         const Set& now = set[u & 1];
         Set& next = set[(u & 1) ^ 1];
-        const int gone = FROM < 0 ? 0 : FROM + u;
         multiply(now, u, [&](int k, int of) {
           const int first = WIDE ? 0 : of / 8;           // the barrier comes after this product
-          if (k == first && gone < kMxStages - 1) {
-            if (gone == 0) mx_wait<(kMxStages - 2) * T::COPIES>();
-            else if (gone == 1) mx_wait<(kMxStages - 3) * T::COPIES>();
+          if (k == first) {
+            if (MORE) mx_wait<(RING - 2) * T::COPIES>();   // and some scales, which a later stage needs
             else mx_wait<0>();
             mx_barrier();
             if (u == T::SPC - 1) read_scales(c + 1, na, nb);
           }
           if (k >= first) {
             const int at = k - first, n = of - first;
-            if (gone < kMxStages - 1) {
 #pragma unroll
-              for (int i = 0; i < READS; ++i)
-                if (i * n / READS == at) read(t + 1, next, i);
-            }
-            if (FROM < 0) {
+            for (int i = 0; i < READS; ++i)
+              if (i * n / READS == at) read(t + 1, next, i);
+            if (MORE) {                                  // stage t + RING, and scales of the chunk after its own
+              constexpr int ITEMS = W + T::COPIES_SC;
 #pragma unroll
-              for (int i = 0; i < T::COPIES; ++i)
-                if (i * n / T::COPIES == at) copy(t + kMxStages, i);
+              for (int i = 0; i < ITEMS; ++i)
+                if (i * n / ITEMS == at) {
+                  if (i < W) copy((uint32_t)(t % RING) * T::STAGE, i);
+                  else copy_scales(c + RING / T::SPC + 1, (u * T::COPIES_SC + i - W) % W);
+                }
             }
           }
           __builtin_amdgcn_sched_barrier(0);
@@ -252,33 +263,39 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
       }
     };
 
-    // the first chunk's scales, then the ring
+    // the scales of the chunks in flight and one more, then the ring
+#pragma unroll 1
+    for (int k = 0; k <= RING / T::SPC; ++k)
 #pragma unroll
-    for (int j = 0; j < W; ++j) mx_copy_scales(gs[j], off4, sc0 + scale_at(j));
+      for (int j = 0; j < W; ++j) copy_scales(k, j);
+#pragma unroll 1
+    for (int t = 0; t < min(RING, stages); ++t)
 #pragma unroll
-    for (int t = 0; t < kMxStages; ++t)
-      if (t < stages) {
-#pragma unroll
-        for (int i = 0; i < T::COPIES; ++i) copy(t, i);
-      }
-    mx_wait<0>();
+      for (int i = 0; i < W; ++i) copy((uint32_t)t * T::STAGE, i);
+    if (stages >= RING) mx_wait<(RING - 1) * T::COPIES>();
+    else mx_wait<0>();
     mx_barrier();
 #pragma unroll
     for (int i = 0; i < READS; ++i) read(0, set[0], i);
     read_scales(0, xa, xb);
-    static_assert(kMxStages == 4, "the last four stages: one chunk or two");
-    const int32_t all = c1 - c0;
     int32_t c = 0;
-    for (; c < all - 4 / T::SPC; ++c) chunk(c, std::integral_constant<int, -1>{});
-    if (T::SPC == 4 || all > 1) chunk(c++, std::integral_constant<int, 0>{});
-    if (T::SPC == 2) chunk(c, std::integral_constant<int, 2>{});
+#pragma unroll 1
+    for (; c < c1 - c0 - RING / T::SPC; ++c) chunk(c, std::true_type{});
+    if constexpr (W == 4) {                      // as a loop of its own it takes more registers than there are
+      static_assert(RING / T::SPC <= 2, "the chunks in flight");
+      if (RING / T::SPC == 1 || c1 - c0 > 1) chunk(c++, std::false_type{});
+      if (RING / T::SPC == 2) chunk(c, std::false_type{});
+    } else {
+#pragma unroll 1
+      for (; c < c1 - c0; ++c) chunk(c, std::false_type{});
+    }
   }
 
-  // Results through LDS, a wave's 32 rows at a time, so that a row goes out in one
-  // run.  Each wave has a place of its own.
+  // Results through LDS, ROWS tiles' rows of a wave at a time, so that a row goes
+  // out in runs of 16 bytes (bf16) a lane.  Each wave has a place of its own.
   mx_wait<0>();
   mx_barrier();
-  constexpr int COLS = 32 * W;
+  constexpr int COLS = 32 * W, ROWS = T::ROWS, ACROSS = COLS / 8;
   float (*hold)[COLS + 4] = reinterpret_cast<float (*)[COLS + 4]>(lds + wave * (T::EPI / 4));
   const int64_t row0 = ((int64_t)strip_a + (wave >> 1) * W) * kMxRows, col0 = ((int64_t)strip_b + (wave & 1) * W) * kMxRows;
   MxProduct o = p;
@@ -289,20 +306,35 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
     o.bias = nullptr;
     o.accumulate = 0;
   }
+  const int c = lane % ACROSS * 8;
+  const MxStore<8> store(o, col0 + c);
+  const bool inside = row0 + 32 * W <= p.a.rows && col0 + COLS <= p.b.rows;   // all of this wave's results
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
+  for (int i = 0; i < W; i += ROWS) {
 #pragma unroll
-    for (int j = 0; j < W; ++j)
+    for (int h = 0; h < ROWS; ++h)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) hold[8 * (e / 4) + 4 * (lane >> 5) + e % 4][32 * j + (lane & 31)] = acc[i][j][e];
+      for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hold[32 * h + 8 * (e / 4) + 4 * (lane >> 5) + e % 4][32 * j + (lane & 31)] = acc[i + h][j][e];
     __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const auto take = [&](int r, float (&y)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = hold[r][c + e];
+    };
+    if (inside) {
 #pragma unroll 4
-    for (int r = lane / (COLS / 4); r < 32; r += 64 / (COLS / 4)) {
-      const int c = lane % (COLS / 4) * 4;
-      const int64_t row = row0 + 32 * i + r, col = col0 + c;
-      if (row < p.a.rows && col < p.b.rows) {
-        const float y[4] = {hold[r][c], hold[r][c + 1], hold[r][c + 2], hold[r][c + 3]};
-        mx_store4(o, row, col, p.b.rows - col, y);
+      for (int r = lane / ACROSS; r < 32 * ROWS; r += 64 / ACROSS) {
+        float y[8];
+        take(r, y);
+        store.whole(row0 + 32 * i + r, y);
+      }
+    } else if (store.left > 0) {
+#pragma unroll 1
+      for (int r = lane / ACROSS; r < 32 * ROWS && row0 + 32 * i + r < p.a.rows; r += 64 / ACROSS) {
+        float y[8];
+        take(r, y);
+        store(row0 + 32 * i + r, y);
       }
     }
     __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -25,7 +25,7 @@ NC_STREAM_KERNEL mx_join(MxProduct p) {
         if (e < left) y[e] += q[e];
     }
   }
-  mx_store4(p, row, col, left, y);
+  MxStore<4>(p, col)(row, y);
 }
 
 }  // namespace

@@ -99,54 +99,72 @@ template <bool WIDE> __device__ __forceinline__ MxScales mx_scales(uint32_t own,
   return s;
 }
 
-// One result: bias, what is there already, rounding to out's type.
-__device__ __forceinline__ float mx_bias(const MxProduct& p, int64_t col) {
-  if (p.bias == nullptr) return 0.0f;
-  return p.out_dtype == NC_BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.bias)[col] << 16)
-                                : static_cast<const float*>(p.bias)[col];
-}
-
-// Four neighbouring results of a row, `left` of them inside the matrix.
-__device__ __forceinline__ void mx_store4(const MxProduct& p, int64_t row, int64_t col, int64_t left, const float (&y)[4]) {
-  float v[4];
+// ---- results ------------------------------------------------------------------------
+// N neighbouring results of rows, columns col .. col + N - 1 of which `left` are
+// inside the matrix: bias (read once), what is there already, rounding to out's
+// type.  The code is short on purpose: it runs once a workgroup, and fetching it
+// anew is what much of it would cost.
+template <int N> struct MxStore {
+  const MxProduct& p;
+  int64_t col, left;
+  float bias[N];
+  __device__ __forceinline__ MxStore(const MxProduct& q, int64_t c) : p(q), col(c), left(q.b.rows - c) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = y[i] + (i < left ? mx_bias(p, col + i) : 0.0f);
-  const int64_t at = row * p.out_stride + col;
-  if (p.out_dtype == NC_BF16) {
-    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-    if (left >= 4) {
-      u32x2 w;
-      if (p.accumulate) {
-        __builtin_memcpy(&w, o, 8);
+    for (int i = 0; i < N; ++i) bias[i] = 0.0f;
+    if (p.bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-      }
-      w = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-      __builtin_memcpy(o, &w, 8);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) {
-          if (p.accumulate) v[i] += __uint_as_float((uint32_t)o[i] << 16);
-          o[i] = (uint16_t)bf16_pair(v[i], 0.0f);
-        }
-    }
-  } else {
-    float* o = static_cast<float*>(p.out) + at;
-    if (left >= 4) {
-      float w[4];
-      if (p.accumulate) {
-        __builtin_memcpy(w, o, 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += w[i];
-      }
-      __builtin_memcpy(o, v, 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) o[i] = p.accumulate ? o[i] + v[i] : v[i];
+      for (int i = 0; i < N; ++i)
+        if (i < left)
+          bias[i] = p.out_dtype == NC_BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.bias)[col + i] << 16)
+                                           : static_cast<const float*>(p.bias)[col + i];
     }
   }
-}
+  // all N inside the matrix
+  __device__ __forceinline__ void whole(int64_t row, float (&y)[N]) const {
+    const int64_t at = row * p.out_stride + col;
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] += bias[i];
+    if (p.out_dtype == NC_BF16) {
+      uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+      uint32_t w[N / 2];
+      if (p.accumulate) {
+        __builtin_memcpy(w, o, 2 * N);
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] += __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+      }
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) w[i] = bf16_pair(y[2 * i], y[2 * i + 1]);
+      __builtin_memcpy(o, w, 2 * N);
+    } else {
+      float* o = static_cast<float*>(p.out) + at;
+      if (p.accumulate) {
+        float w[N];
+        __builtin_memcpy(w, o, 4 * N);
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] += w[i];
+      }
+      __builtin_memcpy(o, y, 4 * N);
+    }
+  }
+  __device__ __forceinline__ void operator()(int64_t row, float (&y)[N]) const {
+    if (left >= N) {
+      whole(row, y);
+    } else {
+      const int64_t at = row * p.out_stride + col;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) {
+          const float v = y[i] + bias[i];
+          if (p.out_dtype == NC_BF16) {
+            uint16_t* o = static_cast<uint16_t*>(p.out) + at + i;
+            *o = (uint16_t)bf16_pair(p.accumulate ? v + __uint_as_float((uint32_t)*o << 16) : v, 0.0f);
+          } else {
+            float* o = static_cast<float*>(p.out) + at + i;
+            *o = p.accumulate ? *o + v : v;
+          }
+        }
+    }
+  }
+};
 
 }  // namespace nc
