@@ -655,7 +655,7 @@ def nc_kv_attention(cache: KvCache, q: torch.Tensor, out: torch.Tensor, q_start:
 
 MX_FMT = {"e2m1": NC_E2M1, "e4m3": NC_E4M3, "e5m2": NC_E5M2}
 ACT = {"silu": NC_ACT_SILU, "gelu": NC_ACT_GELU, "gelu_tanh": NC_ACT_GELU_TANH, "relu2": NC_ACT_RELU2}
-_MX_ELEMENT = {torch.float32: (NC_F32, 4), torch.bfloat16: (NC_BF16, 2)}   # code, bytes of an element
+_MX_DTYPE = {torch.float32: NC_F32, torch.bfloat16: NC_BF16}
 
 
 class MxMatrix:
@@ -708,75 +708,76 @@ def new_mx_matrix(rows: int, cols: int, fmt: str = "e2m1", device="cuda") -> MxM
     return MxMatrix(torch.zeros(mx_bytes(rows, cols, fmt), dtype=torch.uint8, device=device), rows, cols, fmt)
 
 
-def _plane(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, dev: torch.device, out: bool = False) -> NcPlane:
-    """The call's view of a [rows, cols] tensor with adjacent elements; any row stride, without overlap where it is
+def _plane(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype, dev: torch.device, out: bool = False):
+    """Pointer and row stride of a [rows, cols] tensor with adjacent elements; any stride, without overlap where it is
     written."""
-    if t.dtype is not dtype or t.shape != shape or t.device != dev:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} of {t.dtype} on {t.device}, expected {tuple(shape)} of "
-                         f"{dtype} on {dev}")
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.device != dev:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} of {t.dtype} on {t.device}, expected {(rows, cols)} of {dtype} "
+                         f"on {dev}")
     stride, one = t.stride()
-    rows, cols = shape
     if rows < 2:                                 # torch gives an axis of length 1 any stride
         stride = cols
-    if (cols > 1 and one != 1) or (out and stride < cols):
+    if (one != 1 and cols > 1) or (out and stride < cols):
         raise ValueError(f"{name}: strides {t.stride()}: rows of adjacent elements"
                          f"{' that do not overlap' if out else ''} expected")
-    return NcPlane(t.data_ptr(), stride)
+    return t.data_ptr(), stride
 
 
-def _element(t: torch.Tensor, name: str) -> int:
-    code, _ = _MX_ELEMENT.get(t.dtype, (None, 0))
+def _element(dtype: torch.dtype, name: str) -> int:
+    code = _MX_DTYPE.get(dtype)
     if code is None:
-        raise TypeError(f"{name}: dtype {t.dtype} (float32 or bfloat16 expected)")
+        raise TypeError(f"{name}: dtype {dtype} (float32 or bfloat16 expected)")
     return code
 
 
-def _on(*matrices: MxMatrix):
-    """One device for all, a GPU."""
-    dev = matrices[0]._device
-    for m in matrices[1:]:
-        if m._device != dev:
-            raise ValueError(f"matrices on {dev} and {m._device}")
-    if matrices[0]._gpu is None:
+def _one_device(a, b) -> torch.device:
+    """The GPU of two matrices (b may be None)."""
+    dev = a._device
+    if b is not None and b._device != dev:
+        raise ValueError(f"matrices on {dev} and {b._device}")
+    if a._gpu is None:
         raise ValueError("device tensor expected (no CPU path)")
     return dev
 
 
-def _rule(rule) -> int:
-    if rule not in MX_RULE:
-        raise ValueError(f"rule {rule!r}: one of {sorted(MX_RULE)}")
-    return MX_RULE[rule]
+def _named(name, names: dict, what: str) -> int:
+    code = names.get(name)
+    if code is None:
+        raise ValueError(f"{what} {name!r}: one of {sorted(names)}")
+    return code
 
 
 def nc_mx_write(x: torch.Tensor, m: Optional[MxMatrix] = None, t: Optional[MxMatrix] = None, rule="ceil", stream=None):
     """Quantise x [rows, cols] (fp32 or bf16, any row stride) into m, with blocks along its rows, and into t, the
     transposed matrix [cols, rows] with blocks down its columns; one of them or, from one read of x, both."""
-    code, r = _element(x, "x"), _rule(rule)
-    any_ = m if m is not None else t
-    if any_ is None:
+    code, r, md, td = _element(x.dtype, "x"), _named(rule, MX_RULE, "rule"), None, None
+    if m is not None:
+        md, one, rows, cols = m.descriptor, m, m._rows, m._cols   # descriptor first: it looks at data anew
+    if t is not None:
+        td = t.descriptor
+        if m is None:
+            one, rows, cols = t, t._cols, t._rows
+        elif t._cols != rows or t._rows != cols or t._fmt != m._fmt:
+            raise ValueError(f"t: {t.rows} x {t.cols} of {t.fmt}, expected {cols} x {rows} of {m.fmt}")
+    elif m is None:
         raise ValueError("m or t: one matrix at least")
-    md, td = (None if q is None else q.descriptor for q in (m, t))   # first: they look at data anew
-    shape = (m.rows, m.cols) if m is not None else (t.cols, t.rows)
-    if m is not None and t is not None and ((t.cols, t.rows) != shape or t.fmt != m.fmt):
-        raise ValueError(f"t: {t.rows} x {t.cols} of {t.fmt}, expected {m.cols} x {m.rows} of {m.fmt}")
-    dev = _on(*(q for q in (m, t) if q is not None))
-    _kv_call(any_, "nc_mx_write", _lib.load().nc_mx_write, md, td, _plane(x, "x", shape, x.dtype, dev), code, r,
-             _kv_stream(stream, any_._gpu))
+    dev = _one_device(one, t)
+    _kv_call(one, "nc_mx_write", _lib.load().nc_mx_write, md, td, NcPlane(*_plane(x, "x", rows, cols, x.dtype, dev)), code,
+             r, _kv_stream(stream, one._gpu))
 
 
 def nc_mx_read(m: MxMatrix, out: torch.Tensor, stream=None):
     """The matrix's values, as fp32 or bf16 [rows, cols]."""
-    code, d = _element(out, "out"), m.descriptor
-    y = _plane(out, "out", (m.rows, m.cols), out.dtype, _on(m), out=True)
-    _kv_call(m, "nc_mx_read", _lib.load().nc_mx_read, d, y, code, _kv_stream(stream, m._gpu))
+    code, d = _element(out.dtype, "out"), m.descriptor
+    y = _plane(out, "out", m._rows, m._cols, out.dtype, _one_device(m, None), True)
+    _kv_call(m, "nc_mx_read", _lib.load().nc_mx_read, d, NcPlane(*y), code, _kv_stream(stream, m._gpu))
 
 
 def mx_workspace_bytes(rows: int, w: MxMatrix, fmt: Optional[str] = None) -> int:
-    if fmt is not None and fmt not in MX_FMT:
-        raise ValueError(f"fmt {fmt!r}: one of {sorted(MX_FMT)}")
+    code = -1 if fmt is None else _named(fmt, MX_FMT, "fmt")
     if not 0 <= rows <= _I32_MAX:
         raise ValueError(f"rows {rows}: 0 to 2^31 - 1")
-    return int(_lib.load().nc_mx_workspace_bytes(w.descriptor, rows, -1 if fmt is None else MX_FMT[fmt]))
+    return int(_lib.load().nc_mx_workspace_bytes(w.descriptor, rows, code))
 
 
 def new_mx_workspace(rows: int, w: MxMatrix, fmt: Optional[str] = None) -> torch.Tensor:
@@ -785,30 +786,33 @@ def new_mx_workspace(rows: int, w: MxMatrix, fmt: Optional[str] = None) -> torch
     return torch.empty(max(mx_workspace_bytes(rows, w, fmt), 16), dtype=torch.uint8, device=w.device)
 
 
-def _mx_out(out: torch.Tensor, rows: int, w: MxMatrix, bias: Optional[torch.Tensor], accumulate: bool) -> NcMxOut:
-    code = _element(out, "out")
-    p = _plane(out, "out", (rows, w.rows), out.dtype, w._device, out=True)
-    at = None
+def _mx_out(out: torch.Tensor, rows: int, w: MxMatrix, dev: torch.device, bias: Optional[torch.Tensor], accumulate: bool):
+    dt, at, cols = out.dtype, None, w._rows
+    code = _element(dt, "out")
+    p, stride = _plane(out, "out", rows, cols, dt, dev, True)
     if bias is not None:
-        if bias.dtype is not out.dtype or bias.shape != (w.rows,) or bias.device != w._device or not bias.is_contiguous():
+        if bias.dtype is not dt or bias.shape != (cols,) or bias.device != dev or not bias.is_contiguous():
             raise ValueError(f"bias: shape {tuple(bias.shape)} of {bias.dtype} on {bias.device}, expected contiguous "
-                             f"({w.rows},) of {out.dtype} on {w._device}")
+                             f"({cols},) of {dt} on {dev}")
         at = bias.data_ptr()
-    return NcMxOut(p.data, p.stride, code, 1 if accumulate else 0, at)
+    return NcMxOut(p, stride, code, 1 if accumulate else 0, at)
 
 
-def _mx_ws(ws: Optional[torch.Tensor], need: int, w: MxMatrix, stream):
-    """Pointer and size of the workspace; where none is given and some is needed, one from torch on the call's own
-    stream: freed memory is handed out again in that stream's order."""
+def _mx_ws(ws: Optional[torch.Tensor], rows: int, fmt: int, d, dev: torch.device, stream):
+    """Pointer, size and holder of the workspace; where none is given and some is needed, one from torch on the call's
+    own stream: freed memory is handed out again in that stream's order."""
     if ws is not None:
-        if ws.dtype is not torch.uint8 or ws.device != w._device or not ws.is_contiguous():
-            raise ValueError(f"ws: dtype {ws.dtype} on {ws.device}, expected contiguous torch.uint8 on {w._device}")
-    elif need:
-        on = torch.cuda.current_stream(w._device) if stream is None else (
-            stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=w._device))
-        with torch.cuda.stream(on):
-            ws = torch.empty(need, dtype=torch.uint8, device=w._device)
-    return (None, 0, None) if ws is None else (ws.data_ptr(), ws.numel(), ws)
+        if ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: dtype {ws.dtype} on {ws.device}, expected contiguous torch.uint8 on {dev}")
+        return ws.data_ptr(), ws.numel(), ws
+    need = int(_lib.load().nc_mx_workspace_bytes(d, rows, fmt))
+    if not need:
+        return None, 0, None
+    on = torch.cuda.current_stream(dev) if stream is None else (
+        stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev))
+    with torch.cuda.stream(on):
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    return ws.data_ptr(), need, ws
 
 
 def nc_mx_matmul(a: MxMatrix, b: MxMatrix, out: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -816,13 +820,12 @@ def nc_mx_matmul(a: MxMatrix, b: MxMatrix, out: torch.Tensor, bias: Optional[tor
     """out = a b^T (+ bias) (+ out with accumulate): a [rows, k], b [n, k], out [rows, n] fp32 or bf16, bias [n] of
     the same type.  The formats may differ."""
     ad, bd = a.descriptor, b.descriptor
-    if a.cols != b.cols:
+    if a._cols != b._cols:
         raise ValueError(f"a: {a.cols} columns, b has {b.cols}")
-    _on(b, a)
-    o = _mx_out(out, a.rows, b, bias, accumulate)
-    lib = _lib.load()
-    at, n, held = _mx_ws(ws, lib.nc_mx_workspace_bytes(bd, a.rows, -1) if ws is None else 0, b, stream)
-    _kv_call(b, "nc_mx_matmul", lib.nc_mx_matmul, ad, bd, o, at, n, _kv_stream(stream, b._gpu))
+    dev = _one_device(b, a)
+    o = _mx_out(out, a._rows, b, dev, bias, accumulate)
+    at, n, held = _mx_ws(ws, a._rows, -1, bd, dev, stream)
+    _kv_call(b, "nc_mx_matmul", _lib.load().nc_mx_matmul, ad, bd, o, at, n, _kv_stream(stream, b._gpu))
 
 
 def nc_mx_linear(x: torch.Tensor, w: MxMatrix, out: torch.Tensor, fmt: str = "e4m3", rule="ceil",
@@ -830,34 +833,25 @@ def nc_mx_linear(x: torch.Tensor, w: MxMatrix, out: torch.Tensor, fmt: str = "e4
                  stream=None):
     """out = q(x) w^T (+ bias) (+ out): x [rows, k] fp32 or bf16, quantised to `fmt` on the way with blocks along its
     rows; w [n, k]; out [rows, n] fp32 or bf16."""
-    code, r = _element(x, "x"), _rule(rule)
-    if fmt not in MX_FMT:
-        raise ValueError(f"fmt {fmt!r}: one of {sorted(MX_FMT)}")
-    wd = w.descriptor
-    dev = _on(w)
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, {w.cols})")
-    rows = x.shape[0]
-    p = _plane(x, "x", (rows, w.cols), x.dtype, dev)
+    dt, d, shape = x.dtype, w.descriptor, x.shape
+    code, f, r = _element(dt, "x"), _named(fmt, MX_FMT, "fmt"), _named(rule, MX_RULE, "rule")
+    dev = _one_device(w, None)
+    if len(shape) != 2:
+        raise ValueError(f"x: shape {tuple(shape)}, expected (rows, {w.cols})")
+    rows = shape[0]
     if rows > _I32_MAX:
         raise ValueError(f"x: {rows} rows, at most 2^31 - 1")
-    o = _mx_out(out, rows, w, bias, accumulate)
-    lib = _lib.load()
-    at, n, held = _mx_ws(ws, lib.nc_mx_workspace_bytes(wd, rows, MX_FMT[fmt]) if ws is None else 0, w, stream)
-    _kv_call(w, "nc_mx_linear", lib.nc_mx_linear, p, rows, code, MX_FMT[fmt], r, wd, o, at, n, _kv_stream(stream, w._gpu))
+    p = NcPlane(*_plane(x, "x", rows, w._cols, dt, dev))
+    o = _mx_out(out, rows, w, dev, bias, accumulate)
+    at, n, held = _mx_ws(ws, rows, f, d, dev, stream)
+    _kv_call(w, "nc_mx_linear", _lib.load().nc_mx_linear, p, rows, code, f, r, d, o, at, n, _kv_stream(stream, w._gpu))
 
 
 # -- activations that keep their inputs in 8 or 4 bits ----------------------------
 
 
-def _act(act) -> int:
-    if act not in ACT:
-        raise ValueError(f"act {act!r}: one of {sorted(ACT)}")
-    return ACT[act]
-
-
 def _alike(up_q: MxMatrix, gate_q: MxMatrix):
-    if (up_q.rows, up_q.cols, up_q.fmt) != (gate_q.rows, gate_q.cols, gate_q.fmt):
+    if (up_q._rows, up_q._cols, up_q._fmt) != (gate_q._rows, gate_q._cols, gate_q._fmt):
         raise ValueError(f"up_q: {up_q.rows} x {up_q.cols} of {up_q.fmt}, expected {gate_q.rows} x {gate_q.cols} of "
                          f"{gate_q.fmt}")
 
@@ -875,24 +869,28 @@ def nc_act_forward(gate: torch.Tensor, up: Optional[torch.Tensor], y: torch.Tens
     """y = f(gate) * up, or f(gate) where up is None; gate and up [rows, cols] fp32 or bf16 (any row stride: halves of
     one projection will do).  gate_q and up_q, matrices of that shape, keep them for nc_act_backward; without them
     nothing is kept.  act: "silu", "gelu", "gelu_tanh" or "relu2"."""
-    f, code, r = _act(act), _element(gate, "gate"), _rule(rule)
-    if gate.dim() != 2:
-        raise ValueError(f"gate: shape {tuple(gate.shape)}, expected (rows, cols)")
-    shape, dt = gate.shape, gate.dtype
+    dt, shape = gate.dtype, gate.shape
+    f, code, r = _named(act, ACT, "act"), _element(dt, "gate"), _named(rule, MX_RULE, "rule")
+    if len(shape) != 2:
+        raise ValueError(f"gate: shape {tuple(shape)}, expected (rows, cols)")
+    rows, cols = shape
     if (up_q is not None) if gate_q is None else (up_q is None) != (up is None):
         raise ValueError("up_q goes with up and gate_q")
+    gd = ud = None
     if gate_q is None:
-        mx_bytes(*shape, "e4m3")                 # the sizes that a call takes
-    gd, ud = (None if q is None else q.descriptor for q in (gate_q, up_q))
-    at = gate_q if gate_q is not None else _Gpu(gate.device)
-    dev = _on(*(q for q in (at, up_q) if q is not None))
-    if gate_q is not None and (gate_q.rows, gate_q.cols) != tuple(shape):
-        raise ValueError(f"gate_q: {gate_q.rows} x {gate_q.cols}, expected {shape[0]} x {shape[1]}")
-    if up_q is not None:
-        _alike(up_q, gate_q)
-    gp, yp = _plane(gate, "gate", shape, dt, dev), _plane(y, "y", shape, dt, dev, out=True)
-    up_ = None if up is None else _plane(up, "up", shape, dt, dev)
-    _kv_call(at, "nc_act_forward", _lib.load().nc_act_forward, f, *shape, gp, up_, yp, code, gd, ud, r,
+        mx_bytes(rows, cols, "e4m3")             # the sizes that a call takes
+        at = _Gpu(gate.device)
+    else:
+        at, gd = gate_q, gate_q.descriptor
+        if gate_q._rows != rows or gate_q._cols != cols:
+            raise ValueError(f"gate_q: {gate_q.rows} x {gate_q.cols}, expected {rows} x {cols}")
+        if up_q is not None:
+            ud = up_q.descriptor
+            _alike(up_q, gate_q)
+    dev = _one_device(at, up_q)
+    g, o = NcPlane(*_plane(gate, "gate", rows, cols, dt, dev)), NcPlane(*_plane(y, "y", rows, cols, dt, dev, True))
+    u = None if up is None else NcPlane(*_plane(up, "up", rows, cols, dt, dev))
+    _kv_call(at, "nc_act_forward", _lib.load().nc_act_forward, f, rows, cols, g, u, o, code, gd, ud, r,
              _kv_stream(stream, at._gpu))
 
 
@@ -900,15 +898,17 @@ def nc_act_backward(dy: torch.Tensor, gate_q: MxMatrix, up_q: Optional[MxMatrix]
                     dup: Optional[torch.Tensor] = None, act="silu", y: Optional[torch.Tensor] = None, stream=None):
     """The gradients of nc_act_forward from what it kept: dgate = dy u f'(g), dup = dy f(g) (with up_q), g and u the
     kept values; and, where y is given, y = f(g) u again, for the gradient of the weights it was multiplied with."""
-    f, code, dt = _act(act), _element(dy, "dy"), dy.dtype
+    dt = dy.dtype
+    f, code = _named(act, ACT, "act"), _element(dt, "dy")
     if (up_q is None) != (dup is None):
         raise ValueError("dup goes with up_q")
-    gd, ud = gate_q.descriptor, None if up_q is None else up_q.descriptor
-    dev = _on(*(q for q in (gate_q, up_q) if q is not None))
+    gd, ud = gate_q.descriptor, None
     if up_q is not None:
+        ud = up_q.descriptor
         _alike(up_q, gate_q)
-    shape = (gate_q.rows, gate_q.cols)
-    dyp, dgp = _plane(dy, "dy", shape, dt, dev), _plane(dgate, "dgate", shape, dt, dev, out=True)
-    dup_, yp = (None if t is None else _plane(t, n, shape, dt, dev, out=True) for t, n in ((dup, "dup"), (y, "y")))
-    _kv_call(gate_q, "nc_act_backward", _lib.load().nc_act_backward, f, dyp, code, gd, ud, dgp, dup_, yp,
+    dev, rows, cols = _one_device(gate_q, up_q), gate_q._rows, gate_q._cols
+    d, dg = NcPlane(*_plane(dy, "dy", rows, cols, dt, dev)), NcPlane(*_plane(dgate, "dgate", rows, cols, dt, dev, True))
+    du = None if dup is None else NcPlane(*_plane(dup, "dup", rows, cols, dt, dev, True))
+    o = None if y is None else NcPlane(*_plane(y, "y", rows, cols, dt, dev, True))
+    _kv_call(gate_q, "nc_act_backward", _lib.load().nc_act_backward, f, d, code, gd, ud, dg, du, o,
              _kv_stream(stream, gate_q._gpu))

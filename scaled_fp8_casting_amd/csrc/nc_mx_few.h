@@ -14,7 +14,6 @@
 
 namespace nc {
 
-constexpr int kMxFewWaves = 8;
 
 // Rows in place of a matrix.
 enum { kMxNoRows = -1 };   // else their nc_dtype
@@ -59,14 +58,14 @@ __device__ __forceinline__ void mx_few_step(f32x16_t& acc, const MxChunk<FA>& a,
     acc = mx_mma<FA, FB, S>(a.f[S], b.f[S], acc, xa.own, xb.own);
 }
 
-template <int FA, int FB, bool WIDE, int ROWS, int T>
-__global__ void __launch_bounds__(64 * kMxFewWaves) mx_few(MxProduct p) {
+template <int FA, int FB, bool WIDE, int ROWS, int T, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) mx_few(MxProduct p) {
   constexpr bool FUSED = ROWS != kMxNoRows;
   constexpr int DT = FUSED ? ROWS : NC_BF16;
   constexpr int PLACE = mx_chunk_bytes(FA) + kMxScaleBytes;
-  constexpr int HALF = kMxFewWaves / 2, SIDE = 32 * T, LEAD = SIDE + 1;
+  constexpr int HALF = WAVES / 2, SIDE = 32 * T, LEAD = SIDE + 1;
   constexpr int SUMS = HALF * SIDE * LEAD * 4;
-  constexpr int LDS = FUSED && kMxFewWaves * PLACE > SUMS ? kMxFewWaves * PLACE : SUMS;
+  constexpr int LDS = FUSED && WAVES * PLACE > SUMS ? WAVES * PLACE : SUMS;
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = (int)(threadIdx.x & 63);
   const uint32_t across = ((uint32_t)p.b.strips + T - 1) / T;
@@ -111,10 +110,10 @@ __global__ void __launch_bounds__(64 * kMxFewWaves) mx_few(MxProduct p) {
   };
   if constexpr (T == 1) {                        // the next chunk is under way while one is multiplied
     if (wave < chunks) load(wave, a, b);
-    for (int32_t c = wave; c < chunks; c += kMxFewWaves) {
+    for (int32_t c = wave; c < chunks; c += WAVES) {
       MxChunk<FA> na[T];
       MxChunk<FB> nb[T];
-      if (c + kMxFewWaves < chunks) load(c + kMxFewWaves, na, nb);
+      if (c + WAVES < chunks) load(c + WAVES, na, nb);
       if constexpr (FUSED) {
         mx_quantise<FA, DT>(place, p, (int)p.a.rows, (int64_t)c * kMxChunk, lane);
         a[0].load(place, place + mx_chunk_bytes(FA), lane);
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(64 * kMxFewWaves) mx_few(MxProduct p) {
       if constexpr (!FUSED) a[0] = na[0];
     }
   } else {                                       // two waves a SIMD take turns
-    for (int32_t c = wave; c < chunks; c += kMxFewWaves) {
+    for (int32_t c = wave; c < chunks; c += WAVES) {
       load(c, a, b);
       multiply(a, b);
     }
@@ -151,7 +150,7 @@ __global__ void __launch_bounds__(64 * kMxFewWaves) mx_few(MxProduct p) {
   __syncthreads();
   if (wave < HALF) leave(true);
   __syncthreads();
-  for (int i = (int)threadIdx.x; i < SIDE * SIDE / 4; i += 64 * kMxFewWaves) {
+  for (int i = (int)threadIdx.x; i < SIDE * SIDE / 4; i += 64 * WAVES) {
     const int r = i / (SIDE / 4), c = i % (SIDE / 4) * 4;
     const int64_t row = (int64_t)strip_a * kMxRows + r, col = (int64_t)strip_b * kMxRows + c;
     if (row < p.a.rows && col < p.b.rows) {
@@ -165,14 +164,21 @@ __global__ void __launch_bounds__(64 * kMxFewWaves) mx_few(MxProduct p) {
   }
 }
 
-template <int FA, int FB, bool WIDE> hipError_t mx_few_run(const MxProduct& p, int t, hipStream_t stream) {
-  const dim3 block(64 * kMxFewWaves);
-  const dim3 grid(((uint32_t)p.a.strips + t - 1) / t * (((uint32_t)p.b.strips + t - 1) / t));
-  if (t == 2) mx_few<FA, FB, WIDE, kMxNoRows, 2><<<grid, block, 0, stream>>>(p);
-  else if (p.x == nullptr) mx_few<FA, FB, WIDE, kMxNoRows, 1><<<grid, block, 0, stream>>>(p);
-  else if (p.x_dtype == NC_BF16) mx_few<FA, FB, WIDE, NC_BF16, 1><<<grid, block, 0, stream>>>(p);
-  else mx_few<FA, FB, WIDE, NC_F32, 1><<<grid, block, 0, stream>>>(p);
+template <int FA, int FB, bool WIDE, int ROWS, int T, int WAVES> hipError_t mx_few_go(const MxProduct& p, hipStream_t stream) {
+  const dim3 grid(((uint32_t)p.a.strips + T - 1) / T * (((uint32_t)p.b.strips + T - 1) / T));
+  mx_few<FA, FB, WIDE, ROWS, T, WAVES><<<grid, dim3(64 * WAVES), 0, stream>>>(p);
   return hipGetLastError();
+}
+template <int FA, int FB, bool WIDE> hipError_t mx_few_run(const MxProduct& p, int t, hipStream_t stream) {
+  if (p.x == nullptr) return t == 2 ? mx_few_go<FA, FB, WIDE, kMxNoRows, 2, 8>(p, stream) : mx_few_go<FA, FB, WIDE, kMxNoRows, 1, 8>(p, stream);
+  // With a compute unit for each workgroup, sixteen waves take in more at once (1 x
+  // 11008 -> 4096, 4 by 4 bits: 9.2 us against 11.4); two matrices' operands do not fit
+  // their registers (32 x 11008 -> 4096 of 8 by 8 bits: 30 us against 20).
+  // So it is for 8 bits through bf16.
+  constexpr int MORE = WIDE && FB != NC_E2M1 ? 8 : 16;
+  if (p.b.strips <= 256 && p.b.chunks > 8)
+    return p.x_dtype == NC_BF16 ? mx_few_go<FA, FB, WIDE, NC_BF16, 1, MORE>(p, stream) : mx_few_go<FA, FB, WIDE, NC_F32, 1, MORE>(p, stream);
+  return p.x_dtype == NC_BF16 ? mx_few_go<FA, FB, WIDE, NC_BF16, 1, 8>(p, stream) : mx_few_go<FA, FB, WIDE, NC_F32, 1, 8>(p, stream);
 }
 template <int FA, int FB> hipError_t mx_few_launch(const MxProduct& p, int t, hipStream_t stream) {
   if constexpr (FA != NC_E2M1 || FB != NC_E2M1) {
