@@ -139,8 +139,14 @@ template <int DT> __device__ __forceinline__ void store8(void* row, int64_t at, 
 // among them: bit 0 any, bit 1 a NaN.
 template <int DT> __device__ __forceinline__ uint32_t amax8(const Eight<DT>& x, uint32_t& odd) {
   uint32_t a = 0;
+  if constexpr (DT == NC_BF16) {                 // two at a time
+    u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(mag16(x.w[0]), mag16(x.w[1])),
+                                        __builtin_elementwise_max(mag16(x.w[2]), mag16(x.w[3])));
+    a = (uint32_t)max(m.x, m.y) << 16;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, bits_of<DT>(x, i) & kAbsMask);
+    for (int i = 0; i < 8; ++i) a = max(a, x.w[i] & kAbsMask);
+  }
   odd = 0;
   if (a > kMaxFinite) {
     odd = a > kInfBits ? 3u : 1u;

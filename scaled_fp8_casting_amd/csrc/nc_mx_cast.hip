@@ -45,17 +45,21 @@ NC_STREAM_KERNEL mx_write_both(MxMat m, MxMat t, Plane<const void*> x, int rule)
   if (chunk >= (uint32_t)t.chunks) return;
   const int64_t row0 = (int64_t)chunk * kMxChunk + kMxStep * step, col0 = (int64_t)band * kMxChunk;
   const int r = (int)(threadIdx.x >> 3), q = (int)(threadIdx.x & 7);
+  Eight<DT> x8[2][4];                            // all on the way before the first is used
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t row = row0 + 32 * h + r;
-    const bool there = row < rows;
     const uint8_t* p = static_cast<const uint8_t*>(x.p) + row * x.stride * In<DT>::BYTES;
-    Eight<DT> v[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int64_t c = col0 + kMxStep * s + 8 * q;
-      v[s] = load8<DT>(p, c, there ? cols - c : 0);
+      x8[h][s] = load8<DT>(p, c, row < rows ? cols - c : 0);
     }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = row0 + 32 * h + r;
+    const Eight<DT>(&v)[4] = x8[h];
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
