@@ -97,7 +97,7 @@ NC_STREAM_KERNEL act_forward(ActForward a) {
       act_of<ACT>(z[i], f, df);
       y[i] = GATED ? f * w[i] : f;
     }
-    store8<DT>(row_of<DT>(a.y, at.row), at.col(s), a.gate_q.cols - at.col(s), eight_of<DT>(y));
+    store8<DT>(row_of<DT>(a.y, at.row), at.col(s), a.gate_q.cols - at.col(s), eight_of<DT>(y), a.stream);
   }
 }
 
@@ -131,9 +131,9 @@ NC_STREAM_KERNEL act_backward(ActBackward a) {
       dw[i] = d[i] * f;
       y[i] = GATED ? f * w[i] : f;
     }
-    store8<DT>(row_of<DT>(a.dgate, at.row), at.col(s), left, eight_of<DT>(dz));
-    if constexpr (GATED) store8<DT>(row_of<DT>(a.dup, at.row), at.col(s), left, eight_of<DT>(dw));
-    if (a.y.p != nullptr) store8<DT>(row_of<DT>(a.y, at.row), at.col(s), left, eight_of<DT>(y));
+    store8<DT>(row_of<DT>(a.dgate, at.row), at.col(s), left, eight_of<DT>(dz), a.stream);
+    if constexpr (GATED) store8<DT>(row_of<DT>(a.dup, at.row), at.col(s), left, eight_of<DT>(dw), a.stream);
+    if (a.y.p != nullptr) store8<DT>(row_of<DT>(a.y, at.row), at.col(s), left, eight_of<DT>(y), a.stream);
   }
 }
 
@@ -157,18 +157,22 @@ template <typename Fn> hipError_t by_act(int act, int fmt, int dtype, Fn fn) {
 uint32_t grid_of(const MxMat& m) { return (uint32_t)m.strips * (uint32_t)m.chunks; }
 
 struct Forward {
-  const ActForward& a;
+  ActForward a;
   hipStream_t stream;
-  template <int ACT, int FMT, int DT> hipError_t operator()() const {
+  template <int ACT, int FMT, int DT> hipError_t operator()() {
+    a.stream = mx_streams<DT>(a.y, a.gate_q.rows, a.gate_q.cols);
     if (a.up.p != nullptr) act_forward<ACT, FMT, DT, true><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
     else act_forward<ACT, FMT, DT, false><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
     return hipGetLastError();
   }
 };
 struct Backward {
-  const ActBackward& a;
+  ActBackward a;
   hipStream_t stream;
-  template <int ACT, int FMT, int DT> hipError_t operator()() const {
+  template <int ACT, int FMT, int DT> hipError_t operator()() {
+    const int64_t rows = a.gate_q.rows, cols = a.gate_q.cols;
+    a.stream = mx_streams<DT>(a.dgate, rows, cols) && (a.dup.p == nullptr || mx_streams<DT>(a.dup, rows, cols)) &&
+               (a.y.p == nullptr || mx_streams<DT>(a.y, rows, cols));
     if (a.up_q.codes != nullptr) act_backward<ACT, FMT, DT, true><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
     else act_backward<ACT, FMT, DT, false><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
     return hipGetLastError();

@@ -123,7 +123,7 @@ NC_STREAM_KERNEL mx_write_both(MxMat m, MxMat t, Plane<const void*> x, int rule)
 }
 
 template <int FMT, int DT>
-NC_STREAM_KERNEL mx_read(MxMat m, Plane<void*> y) {
+NC_STREAM_KERNEL mx_read(MxMat m, Plane<void*> y, bool stream) {
   const MxLane at(m);
   if (at.row >= m.rows) return;
   uint8_t* row = static_cast<uint8_t*>(y.p) + at.row * y.stride * In<DT>::BYTES;
@@ -143,7 +143,7 @@ NC_STREAM_KERNEL mx_read(MxMat m, Plane<void*> y) {
       decode8<FMT>(c[s], sb, f);
       v = eight_of<DT>(f);
     }
-    store8<DT>(row, at.col(s), m.cols - at.col(s), v);
+    store8<DT>(row, at.col(s), m.cols - at.col(s), v, stream);
   }
 }
 
@@ -181,7 +181,7 @@ struct Read {
   const Plane<void*>& y;
   hipStream_t stream;
   template <int FMT, int DT> hipError_t operator()() const {
-    mx_read<FMT, DT><<<dim3((uint32_t)m.strips * (uint32_t)m.chunks), dim3(kThreads), 0, stream>>>(m, y);
+    mx_read<FMT, DT><<<dim3((uint32_t)m.strips * (uint32_t)m.chunks), dim3(kThreads), 0, stream>>>(m, y, mx_streams<DT>(y, m.rows, m.cols));
     return hipGetLastError();
   }
 };
