@@ -114,7 +114,8 @@ template <int DT> __device__ __forceinline__ Eight<DT> eight_of(const float (&y)
 
 // Results of 32 MiB and more, what the eight L2s hold, are stored past the caches: they
 // would only push out what is being read (8192 x 4096 E4M3 both ways and back 60 us
-// against 67, gated silu over 8192 x 11008 216 against 236).  Smaller ones stay for
+// against 67, gated silu over 8192 x 11008 216 against 236; products 8192^3 E2M1 246
+// against 282).  Smaller ones stay for
 // whoever reads them next.  So do rows that do not start on 16 bytes, whose lines
 // two stores share (3001 x 1357 fp32 26 us, 28 past the caches).
 template <int DT> inline bool mx_streams(const Plane<void*>& y, int64_t rows, int64_t cols) {
@@ -322,6 +323,7 @@ struct MxProduct {
   int64_t out_stride;
   const void* bias;     // nullable, of out's type
   int32_t out_dtype, accumulate;
+  int32_t stream;       // out goes past the caches
   int32_t splits;       // parts of the columns, joined through part
   float* part;
 };

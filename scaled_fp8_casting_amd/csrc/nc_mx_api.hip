@@ -155,6 +155,8 @@ nc_status product(MxProduct& p, int32_t fa, int32_t fb, void* ws, size_t ws_byte
   if (p.x != nullptr) plan = MxPlan{1, 0, 1};
   p.splits = plan.splits;
   p.part = (float*)ws;
+  const Plane<void*> to = {p.out, p.out_stride};
+  p.stream = p.out_dtype == NC_BF16 ? mx_streams<NC_BF16>(to, p.a.rows, p.b.rows) : mx_streams<NC_F32>(to, p.a.rows, p.b.rows);
   if (part_bytes(p.a.rows, p.b.rows, plan.splits) > ws_bytes) return NC_E_WORKSPACE;
   if (plan.t > 0) {
     if (strips_of(p.a.rows) * strips_of(p.b.rows) > plan.t * plan.t * (kMostTiles / 2)) return NC_E_ARG;

@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
     o.out_dtype = NC_F32;
     o.bias = nullptr;
     o.accumulate = 0;
+    o.stream = 0;                                // the join reads them
   }
   const int c = lane % ACROSS * 8;
   const MxStore<8> store(o, col0 + c);

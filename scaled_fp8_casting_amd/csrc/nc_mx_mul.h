@@ -134,6 +134,12 @@ template <int N> struct MxStore {
       }
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) w[i] = bf16_pair(y[2 * i], y[2 * i + 1]);
+      if constexpr (N == 8) {
+        if (p.stream) {
+          __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(o));
+          return;
+        }
+      }
       __builtin_memcpy(o, w, 2 * N);
     } else {
       float* o = static_cast<float*>(p.out) + at;
@@ -142,6 +148,14 @@ template <int N> struct MxStore {
         __builtin_memcpy(w, o, 4 * N);
 #pragma unroll
         for (int i = 0; i < N; ++i) y[i] += w[i];
+      }
+      if constexpr (N == 8) {
+        if (p.stream) {
+          typedef float f32x4_t __attribute__((ext_vector_type(4)));
+          __builtin_nontemporal_store(f32x4_t{y[0], y[1], y[2], y[3]}, reinterpret_cast<f32x4_t*>(o));
+          __builtin_nontemporal_store(f32x4_t{y[4], y[5], y[6], y[7]}, reinterpret_cast<f32x4_t*>(o) + 1);
+          return;
+        }
       }
       __builtin_memcpy(o, y, 4 * N);
     }
