@@ -112,14 +112,15 @@ template <int DT> __device__ __forceinline__ Eight<DT> eight_of(const float (&y)
   return x;
 }
 
-// Results of 32 MiB and more, what the eight L2s hold, are stored past the caches: they
-// would only push out what is being read (8192 x 4096 E4M3 both ways and back 60 us
-// against 67, gated silu over 8192 x 11008 216 against 236; products 8192^3 E2M1 246
-// against 282).  Smaller ones stay for
-// whoever reads them next.  So do rows that do not start on 16 bytes, whose lines
-// two stores share (3001 x 1357 fp32 26 us, 28 past the caches).
+// bf16 results of 32 MiB and more, what the eight L2s hold, are stored past the caches:
+// they would only push out what is being read (8192 x 4096 E4M3 both ways and back 60
+// us against 67, gated silu over 8192 x 11008 216 against 236; products 8192^3 E2M1 241
+// against 245).  Smaller ones stay for whoever reads them next.  So do rows that do not
+// start on 16 bytes, whose lines two stores share (3001 x 1357 fp32 26 us, 28 past the
+// caches), and fp32, eight elements of which take two stores (a product 8192^3 to fp32
+// 272 us, 323 past the caches).
 template <int DT> inline bool mx_streams(const Plane<void*>& y, int64_t rows, int64_t cols) {
-  return rows * cols * In<DT>::BYTES >= ((int64_t)32 << 20) && (((uintptr_t)y.p | (uintptr_t)(y.stride * In<DT>::BYTES)) & 15u) == 0;
+  return DT == NC_BF16 && rows * cols * 2 >= ((int64_t)32 << 20) && (((uintptr_t)y.p | (uintptr_t)(y.stride * 2)) & 15u) == 0;
 }
 
 template <int DT>
@@ -127,13 +128,10 @@ __device__ __forceinline__ void store8(void* row, int64_t at, int64_t left, cons
   constexpr int N = DT == NC_BF16 ? 4 : 8;
   uint8_t* p = static_cast<uint8_t*>(row) + at * In<DT>::BYTES;
   if (left >= 8) {
-    if (stream) {
-#pragma unroll
-      for (int i = 0; i < N; i += 4)
-        __builtin_nontemporal_store(u32x4{x.w[i], x.w[i + 1], x.w[i + 2], x.w[i + 3]}, reinterpret_cast<u32x4*>(p + 4 * i));
-    } else {
+    if (DT == NC_BF16 && stream)
+      __builtin_nontemporal_store(u32x4{x.w[0], x.w[1], x.w[2], x.w[3]}, reinterpret_cast<u32x4*>(p));
+    else
       __builtin_memcpy(p, x.w, 4 * N);
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

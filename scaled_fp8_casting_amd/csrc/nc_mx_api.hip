@@ -105,7 +105,7 @@ struct MxCost {
 };
 constexpr MxCost kCost[4] = {
     {0.00038, 0.105, 0.00080, 0.33, 0.0022, 0.53, 1.95},    // 4 x 4 bits
-    {0.00056, 0.160, 0.00105, 0.45, 0.0031, 1.0, 3.2},      // 8 x 4
+    {0.00056, 0.160, 0.00105, 0.45, 0.0031, 1.0, 2.75},     // 8 x 4
     {0.00105, 0.245, 0.00125, 0.58, 0.0040, 1.05, 3.2},     // 8 x 8
     {0.00098, 0.220, 0.00160, 0.90, 0.0065, 1.7, 1e9},      // through bf16
 };
@@ -155,8 +155,7 @@ nc_status product(MxProduct& p, int32_t fa, int32_t fb, void* ws, size_t ws_byte
   if (p.x != nullptr) plan = MxPlan{1, 0, 1};
   p.splits = plan.splits;
   p.part = (float*)ws;
-  const Plane<void*> to = {p.out, p.out_stride};
-  p.stream = p.out_dtype == NC_BF16 ? mx_streams<NC_BF16>(to, p.a.rows, p.b.rows) : mx_streams<NC_F32>(to, p.a.rows, p.b.rows);
+  p.stream = p.out_dtype == NC_BF16 && mx_streams<NC_BF16>(Plane<void*>{p.out, p.out_stride}, p.a.rows, p.b.rows);
   if (part_bytes(p.a.rows, p.b.rows, plan.splits) > ws_bytes) return NC_E_WORKSPACE;
   if (plan.t > 0) {
     if (strips_of(p.a.rows) * strips_of(p.b.rows) > plan.t * plan.t * (kMostTiles / 2)) return NC_E_ARG;

@@ -149,14 +149,6 @@ template <int N> struct MxStore {
 #pragma unroll
         for (int i = 0; i < N; ++i) y[i] += w[i];
       }
-      if constexpr (N == 8) {
-        if (p.stream) {
-          typedef float f32x4_t __attribute__((ext_vector_type(4)));
-          __builtin_nontemporal_store(f32x4_t{y[0], y[1], y[2], y[3]}, reinterpret_cast<f32x4_t*>(o));
-          __builtin_nontemporal_store(f32x4_t{y[4], y[5], y[6], y[7]}, reinterpret_cast<f32x4_t*>(o) + 1);
-          return;
-        }
-      }
       __builtin_memcpy(o, y, 4 * N);
     }
   }
