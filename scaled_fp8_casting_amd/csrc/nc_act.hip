@@ -13,6 +13,7 @@
 //
 // Each byte moves once, so HBM bandwidth bounds them.
 #include <cfloat>
+#include <type_traits>
 
 #include "nc_mx.h"
 
@@ -57,37 +58,57 @@ template <int DT> __device__ __forceinline__ uint8_t* row_of(const Plane<void*>&
   return static_cast<uint8_t*>(x.p) + row * x.stride * In<DT>::BYTES;
 }
 
-template <int ACT, int FMT, int DT, bool GATED>
+// STEPS: how many of a chunk's four steps a workgroup takes.  One where there would be
+// few workgroups of four: a thread's elements follow each other, and their functions
+// are long.  In us, with four and with one: gelu over 1001 x 1365 fp32 9.5 and 7.2,
+// gelu_tanh's gradient over 100 x 4096 7.1 and 3.6, gelu gated over 4096 x 4096 bf16
+// 38.2 and 36.7, silu gated over 8192 x 11008 159 and 174.
+template <int STEPS> struct ActPart {
+  int s0;
+  MxLane at;
+  __device__ __forceinline__ explicit ActPart(const MxMat& m) : s0(STEPS == 4 ? 0 : (int)(blockIdx.x & 3)), at(m, STEPS == 4 ? blockIdx.x : blockIdx.x >> 2) {}
+  __device__ __forceinline__ void put_scales(const MxMat& m, uint32_t scales) const {
+    if ((at.q & 3) != 0) return;
+    if constexpr (STEPS == 4) *reinterpret_cast<uint32_t*>(m.scales + at.scales()) = scales;
+    else m.scales[at.scales() + s0] = (uint8_t)scales;
+  }
+  __device__ __forceinline__ uint32_t get_scales(const MxMat& m) const {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(m.scales + at.scales());
+    return STEPS == 4 ? w : w >> (8 * s0);
+  }
+};
+
+template <int ACT, int FMT, int DT, bool GATED, int STEPS>
 NC_STREAM_KERNEL act_forward(ActForward a) {
-  const MxLane at(a.gate_q);
+  const ActPart<STEPS> part(a.gate_q);
+  const MxLane& at = part.at;
+  const int s0 = part.s0;
   const bool there = at.row < a.gate_q.rows;
-  Eight<DT> g[4], u[4];
+  Eight<DT> g[STEPS], u[STEPS];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int64_t left = there ? a.gate_q.cols - at.col(s) : 0;
-    g[s] = load8<DT>(row_of<DT>(a.gate, at.row), at.col(s), left);
-    if constexpr (GATED) u[s] = load8<DT>(row_of<DT>(a.up, at.row), at.col(s), left);
+  for (int s = 0; s < STEPS; ++s) {
+    const int64_t left = there ? a.gate_q.cols - at.col(s0 + s) : 0;
+    g[s] = load8<DT>(row_of<DT>(a.gate, at.row), at.col(s0 + s), left);
+    if constexpr (GATED) u[s] = load8<DT>(row_of<DT>(a.up, at.row), at.col(s0 + s), left);
   }
   if (a.gate_q.codes != nullptr) {
     uint32_t sg = 0, su = 0;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < STEPS; ++s) {
       uint32_t sb;
-      put_codes<FMT>(a.gate_q.codes + at.codes<FMT>(s), encode_quad<FMT, DT>(g[s], a.rule, sb));
+      put_codes<FMT>(a.gate_q.codes + at.codes<FMT>(s0 + s), encode_quad<FMT, DT>(g[s], a.rule, sb));
       sg |= sb << (8 * s);
       if constexpr (GATED) {
-        put_codes<FMT>(a.up_q.codes + at.codes<FMT>(s), encode_quad<FMT, DT>(u[s], a.rule, sb));
+        put_codes<FMT>(a.up_q.codes + at.codes<FMT>(s0 + s), encode_quad<FMT, DT>(u[s], a.rule, sb));
         su |= sb << (8 * s);
       }
     }
-    if ((at.q & 3) == 0) {
-      *reinterpret_cast<uint32_t*>(a.gate_q.scales + at.scales()) = sg;
-      if constexpr (GATED) *reinterpret_cast<uint32_t*>(a.up_q.scales + at.scales()) = su;
-    }
+    part.put_scales(a.gate_q, sg);
+    if constexpr (GATED) part.put_scales(a.up_q, su);
   }
   if (!there) return;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < STEPS; ++s) {
     float z[8], w[8], y[8];
     floats<DT>(g[s], z);
     if constexpr (GATED) floats<DT>(u[s], w);
@@ -97,28 +118,30 @@ NC_STREAM_KERNEL act_forward(ActForward a) {
       act_of<ACT>(z[i], f, df);
       y[i] = GATED ? f * w[i] : f;
     }
-    store8<DT>(row_of<DT>(a.y, at.row), at.col(s), a.gate_q.cols - at.col(s), eight_of<DT>(y), a.stream);
+    store8<DT>(row_of<DT>(a.y, at.row), at.col(s0 + s), a.gate_q.cols - at.col(s0 + s), eight_of<DT>(y), a.stream);
   }
 }
 
-template <int ACT, int FMT, int DT, bool GATED>
+template <int ACT, int FMT, int DT, bool GATED, int STEPS>
 NC_STREAM_KERNEL act_backward(ActBackward a) {
-  const MxLane at(a.gate_q);
+  const ActPart<STEPS> part(a.gate_q);
+  const MxLane& at = part.at;
+  const int s0 = part.s0;
   if (at.row >= a.gate_q.rows) return;
-  Eight<DT> dy[4];
-  u32x2 g[4], u[4];
+  Eight<DT> dy[STEPS];
+  u32x2 g[STEPS], u[STEPS];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    dy[s] = load8<DT>(row_of<DT>(a.dy, at.row), at.col(s), a.gate_q.cols - at.col(s));
-    g[s] = get_codes<FMT>(a.gate_q.codes + at.codes<FMT>(s));
-    if constexpr (GATED) u[s] = get_codes<FMT>(a.up_q.codes + at.codes<FMT>(s));
+  for (int s = 0; s < STEPS; ++s) {
+    dy[s] = load8<DT>(row_of<DT>(a.dy, at.row), at.col(s0 + s), a.gate_q.cols - at.col(s0 + s));
+    g[s] = get_codes<FMT>(a.gate_q.codes + at.codes<FMT>(s0 + s));
+    if constexpr (GATED) u[s] = get_codes<FMT>(a.up_q.codes + at.codes<FMT>(s0 + s));
   }
-  const uint32_t sg = *reinterpret_cast<const uint32_t*>(a.gate_q.scales + at.scales());
+  const uint32_t sg = part.get_scales(a.gate_q);
   uint32_t su = 0;
-  if constexpr (GATED) su = *reinterpret_cast<const uint32_t*>(a.up_q.scales + at.scales());
+  if constexpr (GATED) su = part.get_scales(a.up_q);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int64_t left = a.gate_q.cols - at.col(s);
+  for (int s = 0; s < STEPS; ++s) {
+    const int64_t col = at.col(s0 + s), left = a.gate_q.cols - col;
     float d[8], z[8], w[8], dz[8], dw[8], y[8];
     floats<DT>(dy[s], d);
     decode8<FMT>(g[s], (sg >> (8 * s)) & 255u, z);
@@ -131,9 +154,9 @@ NC_STREAM_KERNEL act_backward(ActBackward a) {
       dw[i] = d[i] * f;
       y[i] = GATED ? f * w[i] : f;
     }
-    store8<DT>(row_of<DT>(a.dgate, at.row), at.col(s), left, eight_of<DT>(dz), a.stream);
-    if constexpr (GATED) store8<DT>(row_of<DT>(a.dup, at.row), at.col(s), left, eight_of<DT>(dw), a.stream);
-    if (a.y.p != nullptr) store8<DT>(row_of<DT>(a.y, at.row), at.col(s), left, eight_of<DT>(y), a.stream);
+    store8<DT>(row_of<DT>(a.dgate, at.row), col, left, eight_of<DT>(dz), a.stream);
+    if constexpr (GATED) store8<DT>(row_of<DT>(a.dup, at.row), col, left, eight_of<DT>(dw), a.stream);
+    if (a.y.p != nullptr) store8<DT>(row_of<DT>(a.y, at.row), col, left, eight_of<DT>(y), a.stream);
   }
 }
 
@@ -154,15 +177,24 @@ template <typename Fn> hipError_t by_act(int act, int fmt, int dtype, Fn fn) {
   return hipErrorInvalidValue;
 }
 
-uint32_t grid_of(const MxMat& m) { return (uint32_t)m.strips * (uint32_t)m.chunks; }
+constexpr uint32_t kFewChunks = 4096;
+
+// fn(steps of a workgroup as a constant, workgroups)
+template <typename Fn> void by_steps(const MxMat& m, Fn fn) {
+  const uint32_t chunks = (uint32_t)m.strips * (uint32_t)m.chunks;
+  if (chunks < kFewChunks) fn(std::integral_constant<int, 1>{}, dim3(4 * chunks));
+  else fn(std::integral_constant<int, 4>{}, dim3(chunks));
+}
 
 struct Forward {
   ActForward a;
   hipStream_t stream;
   template <int ACT, int FMT, int DT> hipError_t operator()() {
     a.stream = mx_streams<DT>(a.y, a.gate_q.rows, a.gate_q.cols);
-    if (a.up.p != nullptr) act_forward<ACT, FMT, DT, true><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
-    else act_forward<ACT, FMT, DT, false><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
+    by_steps(a.gate_q, [&](auto steps, dim3 grid) {
+      if (a.up.p != nullptr) act_forward<ACT, FMT, DT, true, decltype(steps)::value><<<grid, dim3(kThreads), 0, stream>>>(a);
+      else act_forward<ACT, FMT, DT, false, decltype(steps)::value><<<grid, dim3(kThreads), 0, stream>>>(a);
+    });
     return hipGetLastError();
   }
 };
@@ -173,8 +205,10 @@ struct Backward {
     const int64_t rows = a.gate_q.rows, cols = a.gate_q.cols;
     a.stream = mx_streams<DT>(a.dgate, rows, cols) && (a.dup.p == nullptr || mx_streams<DT>(a.dup, rows, cols)) &&
                (a.y.p == nullptr || mx_streams<DT>(a.y, rows, cols));
-    if (a.up_q.codes != nullptr) act_backward<ACT, FMT, DT, true><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
-    else act_backward<ACT, FMT, DT, false><<<dim3(grid_of(a.gate_q)), dim3(kThreads), 0, stream>>>(a);
+    by_steps(a.gate_q, [&](auto steps, dim3 grid) {
+      if (a.up_q.codes != nullptr) act_backward<ACT, FMT, DT, true, decltype(steps)::value><<<grid, dim3(kThreads), 0, stream>>>(a);
+      else act_backward<ACT, FMT, DT, false, decltype(steps)::value><<<grid, dim3(kThreads), 0, stream>>>(a);
+    });
     return hipGetLastError();
   }
 };

@@ -263,13 +263,13 @@ struct MxLane {
   int r, q;            // row of the strip; which eight of a step's 64 columns
   int64_t row, col0;   // row of the matrix, first column of the chunk
   int64_t tile;        // strip * chunks + chunk
-  __device__ __forceinline__ explicit MxLane(const MxMat& m) {
-    const uint32_t strip = blockIdx.x / (uint32_t)m.chunks, chunk = blockIdx.x % (uint32_t)m.chunks;
+  __device__ __forceinline__ explicit MxLane(const MxMat& m, uint32_t at = blockIdx.x) {
+    const uint32_t strip = at / (uint32_t)m.chunks, chunk = at % (uint32_t)m.chunks;
     r = (int)(threadIdx.x >> 3);
     q = (int)(threadIdx.x & 7);
     row = (int64_t)strip * kMxRows + r;
     col0 = (int64_t)chunk * kMxChunk;
-    tile = (int64_t)blockIdx.x;
+    tile = (int64_t)at;
   }
   __device__ __forceinline__ int64_t col(int step) const { return col0 + kMxStep * step + 8 * q; }
   // byte of this lane's eight codes of a step, in the matrix's codes; of its scales
