@@ -7,21 +7,27 @@
 // from memory to LDS once for the workgroup and from LDS to registers once for each
 // wave that multiplies it; W = 4 reads 64 bytes of LDS for 8 matrix instructions.
 //
-// The copies into LDS are asynchronous and take no registers.  RING stages of them
+// The copies into LDS are asynchronous and take no registers.  kMxRing stages of them
 // are in flight in as many slots of LDS:
 //
 //   stage s:  start multiplying stage s, whose operands are in registers
 //             wait until the copies of stage s + 1 have landed (all waves: barrier)
 //             between the other products, one by one: read stage s + 1 from LDS into
-//               the other set of registers, and start the copies of stage s + RING
+//               the other set of registers, and start the copies of stage s + kMxRing
 //               into the slot of stage s, which all waves had read before the barrier
 //
 // so the matrix units have work at the barrier and beside the reads, and a copy has
-// RING - 1 stages to arrive (8 slots of W = 2 in place of 4 gained nothing).  Issued in one go, the copies and reads of a stage
-// held the products up for as long as memory took to accept them (8192^3 E4M3: 543
-// us, the matrix units busy for 49% of it).  Layout in LDS is that in memory, the instruction's
-// order: a wave's reads are runs of 1 KiB and meet no bank twice.  Scales go the
-// same way, a dword a lane and chunk, a chunk ahead of their codes.
+// kMxRing - 1 stages to arrive (8 slots of W = 2 in place of 4 gained nothing).  Issued
+// in one go, the copies and reads of a stage held the products up for as long as
+// memory took to accept them (8192^3 E4M3: 543 us, the matrix units busy for 49% of
+// it).  Layout in LDS is that in memory, the instruction's order: a wave's reads are
+// runs of 1 KiB and meet no bank twice.  Scales go the same way, a dword a lane and
+// chunk, a chunk ahead of their codes.
+//
+// What bounds it is power: with all compute units at the products alone the clock
+// is 1.46 GHz (E2M1), and the copies and reads take a third of the time more
+// (4096 x 4096 x 16384 E2M1: a stage 0.96 us, 0.70 with the products alone).  8192^3:
+// E2M1 241 us, 4.6 PFLOP/s; E4M3 375 us, 2.9; to fp32 through bf16 890 us.
 #pragma once
 
 #include <type_traits>
@@ -30,21 +36,21 @@
 
 namespace nc {
 
+constexpr int kMxRing = 4;         // stages in flight, and slots
 
-// A copy of one or two KiB from memory to LDS, 16 bytes a lane from base + off; at:
-// byte of LDS of the first lane's.  Written as assembly because the compiler waits for all
-// copies in flight before any read of LDS; waiting is the caller's.  It has no
-// result that a register would have to be kept for.  M0 holds the LDS address (the
-// compiler never leaves a value in it, and nothing else here uses it), and
-// its write needs a wait state before the use.
-// Base and place are the wave's (the same in every lane), which the compiler does not
-// always see.
+// A wave's address, the same in every lane, which the compiler does not always see.
 __device__ __forceinline__ const uint8_t* mx_uniform(const uint8_t* p) {
   const uint64_t b = (uint64_t)(uintptr_t)p;
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b), hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
   return reinterpret_cast<const uint8_t*>((uintptr_t)((uint64_t)hi << 32 | lo));
 }
-// The instruction's offset counts in memory and in LDS.
+// A copy of one or two KiB from memory to LDS, 16 bytes a lane from base + off; at:
+// byte of LDS of the first lane's.  Written as assembly because the compiler waits
+// for all copies in flight before any read of LDS; waiting is the caller's.  It has
+// no result that a register would have to be kept for.  M0 holds the LDS address (the
+// compiler never leaves a value in it, and nothing else here uses it), and its write
+// needs a wait state before the use.  The instruction's offset counts in memory and
+// in LDS.
 template <int UNITS> __device__ __forceinline__ void mx_copy(const uint8_t* base, uint32_t off, uint32_t at) {
   const int m0 = __builtin_amdgcn_readfirstlane((int)at);
   if constexpr (UNITS == 2)
@@ -64,8 +70,6 @@ __device__ __forceinline__ void mx_barrier() {
   __asm__ volatile("" ::: "memory");
 }
 
-constexpr int RING = 4;            // stages in flight, and slots
-
 template <int FA, int FB, int W> struct MxTile {
   static constexpr int STEPS = FA == NC_E2M1 && FB == NC_E2M1 ? 2 : 1;     // of a stage
   static constexpr int SPC = 4 / STEPS;                                    // stages of a chunk
@@ -74,7 +78,7 @@ template <int FA, int FB, int W> struct MxTile {
   static constexpr int STAGE = STRIPS * (UA + UB) * 1024;
   static constexpr int SCALES = 2 * STRIPS * kMxScaleBytes;                // of a chunk
   static constexpr int SLOTS = 4;                                          // chunks of scales: those of the stages in flight and more ahead
-  static constexpr int LDS = RING * STAGE + SLOTS * SCALES;
+  static constexpr int LDS = kMxRing * STAGE + SLOTS * SCALES;
   static constexpr int COPIES_SC = (W + SPC - 1) / SPC;                    // copies of scales of a wave and stage
   static constexpr int COPIES = W / 2 * (UA + UB);                         // other copies of a wave and stage
   static constexpr int ROW_EPI = 4 * 32 * (32 * W + 4) * 4;                // a row of tiles of each wave, on its way out
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
     gs[W / 2 + i] = p.b.scales + sb * kMxScaleBytes;
   }
   const uint32_t off16 = (uint32_t)lane * 16, off4 = (uint32_t)lane * 4;
-  const uint32_t codes0 = lds0 + (uint32_t)wave * (W / 2) * (T::UA * 1024), sc0 = lds0 + RING * T::STAGE + (uint32_t)wave * (W / 2) * kMxScaleBytes;
+  const uint32_t codes0 = lds0 + (uint32_t)wave * (W / 2) * (T::UA * 1024), sc0 = lds0 + kMxRing * T::STAGE + (uint32_t)wave * (W / 2) * kMxScaleBytes;
   // the i-th of this wave's strips, of a, then of b, in the slot at `slot`
   const auto copy = [&](uint32_t slot, int i) {
     if (i < W / 2) {
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
     constexpr int READS = W * (T::UA + T::UB);
     // the i-th read of a stage: in the order in which the products take them
     const auto read = [&](int32_t t, Set& f, int i) {
-      const uint8_t* at = lds + (t % RING) * T::STAGE + lane * 16;
+      const uint8_t* at = lds + (t % kMxRing) * T::STAGE + lane * 16;
       if (i < W * T::UB) f.b[i % W][i / W] = *reinterpret_cast<const u32x4*>(at + T::STRIPS * T::UA * 1024 + (wb * W + i % W) * (T::UB * 1024) + i / W * 1024);
       else f.a[(i - W * T::UB) % W][(i - W * T::UB) / W] = *reinterpret_cast<const u32x4*>(at + (wa * W + (i - W * T::UB) % W) * (T::UA * 1024) + (i - W * T::UB) / W * 1024);
     };
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
       return r;
     };
     const auto read_scales = [&](int32_t c, uint32_t (&a)[W], uint32_t (&b)[W]) {
-      const uint8_t* at = lds + RING * T::STAGE + (c % T::SLOTS) * T::SCALES + lane * 4;
+      const uint8_t* at = lds + kMxRing * T::STAGE + (c % T::SLOTS) * T::SCALES + lane * 4;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         a[i] = *reinterpret_cast<const uint32_t*>(at + (wa * W + i) * kMxScaleBytes);
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
         multiply(now, u, [&](int k, int of) {
           const int first = WIDE ? 0 : of / 8;           // the barrier comes after this product
           if (k == first) {
-            if (MORE) mx_wait<(RING - 2) * T::COPIES>();   // and some scales, which a later stage needs
+            if (MORE) mx_wait<(kMxRing - 2) * T::COPIES>();   // and some scales, which a later stage needs
             else mx_wait<0>();
             mx_barrier();
             if (u == T::SPC - 1) read_scales(c + 1, na, nb);
@@ -241,13 +245,13 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
 #pragma unroll
             for (int i = 0; i < READS; ++i)
               if (i * n / READS == at) read(t + 1, next, i);
-            if (MORE) {                                  // stage t + RING, and scales of the chunk after its own
+            if (MORE) {                                  // stage t + kMxRing, and scales of the chunk after its own
               constexpr int ITEMS = W + T::COPIES_SC;
 #pragma unroll
               for (int i = 0; i < ITEMS; ++i)
                 if (i * n / ITEMS == at) {
-                  if (i < W) copy((uint32_t)(t % RING) * T::STAGE, i);
-                  else copy_scales(c + RING / T::SPC + 1, (u * T::COPIES_SC + i - W) % W);
+                  if (i < W) copy((uint32_t)(t % kMxRing) * T::STAGE, i);
+                  else copy_scales(c + kMxRing / T::SPC + 1, (u * T::COPIES_SC + i - W) % W);
                 }
             }
           }
@@ -265,14 +269,14 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
 
     // the scales of the chunks in flight and one more, then the ring
 #pragma unroll 1
-    for (int k = 0; k <= RING / T::SPC; ++k)
+    for (int k = 0; k <= kMxRing / T::SPC; ++k)
 #pragma unroll
       for (int j = 0; j < W; ++j) copy_scales(k, j);
 #pragma unroll 1
-    for (int t = 0; t < min(RING, stages); ++t)
+    for (int t = 0; t < min(kMxRing, stages); ++t)
 #pragma unroll
       for (int i = 0; i < W; ++i) copy((uint32_t)t * T::STAGE, i);
-    if (stages >= RING) mx_wait<(RING - 1) * T::COPIES>();
+    if (stages >= kMxRing) mx_wait<(kMxRing - 1) * T::COPIES>();
     else mx_wait<0>();
     mx_barrier();
 #pragma unroll
@@ -280,11 +284,11 @@ __global__ void __launch_bounds__(256, W == 4 ? 1 : 2) mx_many(MxProduct p) {
     read_scales(0, xa, xb);
     int32_t c = 0;
 #pragma unroll 1
-    for (; c < c1 - c0 - RING / T::SPC; ++c) chunk(c, std::true_type{});
+    for (; c < c1 - c0 - kMxRing / T::SPC; ++c) chunk(c, std::true_type{});
     if constexpr (W == 4) {                      // as a loop of its own it takes more registers than there are
-      static_assert(RING / T::SPC <= 2, "the chunks in flight");
-      if (RING / T::SPC == 1 || c1 - c0 > 1) chunk(c++, std::false_type{});
-      if (RING / T::SPC == 2) chunk(c, std::false_type{});
+      static_assert(kMxRing / T::SPC <= 2, "the chunks in flight");
+      if (kMxRing / T::SPC == 1 || c1 - c0 > 1) chunk(c++, std::false_type{});
+      if (kMxRing / T::SPC == 2) chunk(c, std::false_type{});
     } else {
 #pragma unroll 1
       for (; c < c1 - c0; ++c) chunk(c, std::false_type{});
