@@ -537,8 +537,9 @@ typedef struct {
  * to multiples of that).  bf16 results of 8-bit operands come from the scaled
  * matrix instruction, which of eight neighbouring columns' products drops what lies
  * below 2^-13 of the largest.  With no columns the sum is 0.
- * NC_E_ARG where (rows of a / 128) * (rows of b / 128), each rounded up, passes 2^24
- * (2^23 tiles of 64 x 64 where there are no columns).
+ * NC_E_ARG where the results have 2^24 or more tiles of 128 x 128 (with no columns:
+ * 2^23 of 64 x 64; nc_mx_linear of few rows: 2^23 of 32 x 32), the last of each side
+ * counted in full.
  *
  * ws: nc_mx_workspace_bytes() bytes, 16-byte aligned, no initialisation; NULL
  * where that is 0.  Long sums are cut along the columns over the workgroups and

@@ -88,7 +88,8 @@ constexpr int64_t kSplitChunks = 4;              // fewest chunks of a split
 // part for each workgroup and of what one compute unit takes for its share of them.
 // Fitted to 17 sizes of 33 .. 2048 x 256 .. 11008 x 1024 .. 16384 in each class and
 // checked at 70 drawn ones (2 .. 8192 x 40 .. 11008 x 70 .. 16384): the choice was
-// within 10% of the fastest in all but those where a launch is most of the time.
+// within 10% of the fastest in all but those where a launch is most of the time and
+// one at 16% (253 x 9025 x 9741 E4M3 x E2M1: 47 us against 40.5 in 3 splits).
 // Some of them, in us (1 strip, 2 strips, 128 a side, 256 a side, 128 in 4 splits):
 //   E2M1 x E2M1    64 x 4096 x 4096    5.6   9.5  12.4          12.0
 //                 512 x 4096 x 4096   18.1  13.4  13.6   27.7   26.6
@@ -158,7 +159,8 @@ nc_status product(MxProduct& p, int32_t fa, int32_t fb, void* ws, size_t ws_byte
   p.stream = p.out_dtype == NC_BF16 && mx_streams<NC_BF16>(Plane<void*>{p.out, p.out_stride}, p.a.rows, p.b.rows);
   if (part_bytes(p.a.rows, p.b.rows, plan.splits) > ws_bytes) return NC_E_WORKSPACE;
   if (plan.t > 0) {
-    if (strips_of(p.a.rows) * strips_of(p.b.rows) > plan.t * plan.t * (kMostTiles / 2)) return NC_E_ARG;
+    const int64_t side = 32 * plan.t;
+    if (((p.a.rows + side - 1) / side) * ((p.b.rows + side - 1) / side) > kMostTiles / 2) return NC_E_ARG;   // 512 threads
     return hip_status(launch_mx_few(p, fa, fb, plan.t, stream));
   }
   if (((p.a.rows + 127) / 128) * ((p.b.rows + 127) / 128) > kMostTiles) return NC_E_ARG;

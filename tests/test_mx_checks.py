@@ -335,3 +335,13 @@ def test_oracle_activations():
         got, df, _, _ = mx.act(z.detach().numpy(), kind)
         np.testing.assert_allclose(got, y.detach().numpy(), rtol=1e-12, atol=1e-15)
         np.testing.assert_allclose(df, d.numpy(), rtol=1e-9, atol=1e-12)
+
+
+# More workgroups than a launch has, where a strip or a tile is not full: 600000001 rows
+# of b are 18750001 strips, 9375001 tiles of 64 (more than 2^23), with one row of a.
+def test_products_past_a_launch(lib):
+    rows = 600000001
+    none, one = matrix(rows=rows, cols=0, data=None), matrix(rows=1, cols=0, data=None)
+    assert lib.nc_mx_matmul(one, none, out(stride=rows), None, 0, None) == _lib.NC_E_ARG
+    assert lib.nc_mx_matmul(none, one, out(stride=1), None, 0, None) == _lib.NC_E_ARG
+    assert lib.nc_mx_linear(None, 1, 1, 0, 2, none, out(stride=rows), A, W, None) == _lib.NC_E_ARG
