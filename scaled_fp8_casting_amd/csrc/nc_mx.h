@@ -35,7 +35,7 @@ constexpr int mx_bits(int fmt) { return fmt == NC_E2M1 ? 4 : 8; }
 constexpr int mx_step_bytes(int fmt) { return kMxRows * kMxStep * mx_bits(fmt) / 8; }
 constexpr int mx_chunk_bytes(int fmt) { return 4 * mx_step_bytes(fmt); }
 constexpr int kMxScaleBytes = 256;   // of a strip and chunk
-constexpr int kMxFusedRows = 6;      // unquantised rows that the few-row product quantises itself
+constexpr int kMxFusedRows = 8;      // unquantised rows that the few-row product quantises itself
 
 // A plane of fp32 or bf16 elements: row i starts at p + i * stride elements.
 template <typename P> struct Plane {

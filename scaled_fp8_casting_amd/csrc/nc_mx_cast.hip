@@ -1,7 +1,7 @@
 // Writing matrices of MX blocks and reading them back.
 //
-// Both move each byte once, so HBM bandwidth bounds them: 8192 x 11008 bf16 to E4M3 54
-// us (5.0 TB/s) and back 45 (6.1), 8192 x 4096 both ways 29 us (4.7).
+// Both move each byte once, so HBM bandwidth bounds them: 8192 x 11008 bf16 to E4M3 55
+// us (4.9 TB/s) and back 45.5 (6.0), 8192 x 4096 both ways 29 us (4.7).
 #include "nc_mx.h"
 
 namespace nc {

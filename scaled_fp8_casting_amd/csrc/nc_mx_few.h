@@ -7,12 +7,19 @@
 // Up to kMxFusedRows unquantised rows (a linear layer's) are quantised on the way:
 // each wave turns the columns of its own chunk into codes, in a place of its own in
 // LDS where they lie as in a matrix.  Every workgroup does it again, which costs
-// more the more rows there are; a kernel of its own writes more rows first (4096 ->
-// 11008, E2M1: 6 rows 10.4 us against 12.0, 8 rows 11.4 and 11.6, 16 rows 15.9 and
-// 11.6; 11008 -> 4096: 6 rows 12.0 and 13.3).
+// more the more rows there are; a kernel of its own writes more rows first.  In us,
+// quantised on the way and first, bf16 rows to E2M1 or E4M3 against E2M1 weights,
+// replayed from a graph over twelve matrices:
+//                            6 rows        8            12           16
+//   E2M1   4096 ->  4096    5.9   7.6    6.3   7.4    7.4   7.5    8.2   7.4
+//          4096 -> 11008   10.3  11.9   11.0  11.4   13.2  11.8   15.3  11.5
+//         11008 ->  4096   11.8  13.2   13.0  12.9   15.4  13.3   17.6  12.7
+//   E4M3   4096 ->  4096    6.0   8.1    6.5   8.1    7.5   8.2    8.4   8.1
+//          4096 -> 11008   10.6  13.0   11.3  12.5   13.7  13.0   15.6  12.6
+//         11008 ->  4096   11.8  15.2   12.9  14.9   15.6  15.3   17.9  14.9
 //
-// 1 x 4096 -> 4096 5.6 us (8.9 MB; the launch and two trips to memory), 24 x 4096 ->
-// 11008 7.1 us behind a write of 3.4 (24 MB at 3.4 TB/s).
+// 1 x 4096 E4M3 -> 4096 E2M1 takes 5.6 us (8.9 MB of weights; the launch and two trips
+// to memory), 24 x 4096 -> 11008 E2M1 7.1 behind a write of 3.4 (24 MB at 3.4 TB/s).
 #pragma once
 
 #include "nc_mx_mul.h"

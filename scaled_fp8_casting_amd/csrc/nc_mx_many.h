@@ -5,7 +5,7 @@
 // 128 x 128, two workgroups a compute unit).  Every operand byte of a stage -- two
 // steps of 64 columns of two E2M1 operands, one step where one has 8 bits -- goes
 // from memory to LDS once for the workgroup and from LDS to registers once for each
-// wave that multiplies it; W = 4 reads 64 bytes of LDS for 8 matrix instructions.
+// wave that multiplies it; W = 4 reads 8 operands of 32 x 64 for 16 matrix instructions.
 //
 // The copies into LDS are asynchronous and take no registers.  kMxRing stages of them
 // are in flight in as many slots of LDS:
@@ -26,8 +26,9 @@
 //
 // What bounds it is power: with all compute units at the products alone the clock
 // is 1.46 GHz (E2M1), and the copies and reads take a third of the time more
-// (4096 x 4096 x 16384 E2M1: a stage 0.96 us, 0.70 with the products alone).  8192^3:
-// E2M1 241 us, 4.6 PFLOP/s; E4M3 375 us, 2.9; to fp32 through bf16 890 us.
+// (4096 x 4096 x 16384 E2M1: a stage 0.96 us, 0.70 with the products alone).  8192^3
+// once the power control has settled: E2M1 241 .. 247 us, 4.5 PFLOP/s; E4M3 375 .. 383,
+// 2.9; to fp32 through bf16 890 .. 907.  The first 8 ms of a load: 274, 440, 990.
 #pragma once
 
 #include <type_traits>

@@ -161,3 +161,20 @@ def test_a_matrix_with_itself():
     nc.nc_mx_matmul(a, a, out)
     close(out, *product(x, x, "e4m3", "e4m3", "fp32"))
     assert torch.equal(out, out.T)
+
+
+@pytest.mark.parametrize("rows", [5, 6, 7, 8, 9])
+@pytest.mark.parametrize("fa,fb", [("e2m1", "e2m1"), ("e4m3", "e2m1"), ("e4m3", "e4m3"), ("e5m2", "e4m3")])
+def test_linear_where_rows_are_written_first(fa, fb, rows):
+    """Either side of the number of rows that a product quantises itself, over eight chunks of columns and more (sixteen
+    waves), with rows past the last that a stale place in LDS could reach, and a workspace for other rows."""
+    rng = np.random.default_rng(6)
+    for n, k in [(40, 2048), (300, 2500), (33, 4100)]:
+        x, w = data(rng, rows, k, "bf16", tail=0.7), data(rng, n, k, "bf16")
+        wq, xg = written(w, fb), x.cuda()
+        for dtype in ("bf16", "fp32"):
+            out, again = blank(rows, n, dtype), blank(rows, n, dtype)
+            nc.nc_mx_linear(xg, wq, out, fmt=fa)
+            close(out, *product(x, w, fa, fb, dtype))
+            nc.nc_mx_linear(xg, wq, again, fmt=fa, ws=nc.new_mx_workspace(200, wq, fa))
+            assert torch.equal(again, out)
