@@ -577,7 +577,9 @@ nc_status nc_act_forward(nc_act act, int64_t rows, int64_t cols, const nc_plane 
 /* Backward from what was kept: with g and u the values of gate_q and up_q
  * (nullable),  dgate = dy u f'(g)  and  dup = dy f(g)  (dup goes with up_q), and
  * where y is given (nullable) y = f(g) u again, for the gradient of the weights
- * that y was multiplied with.  dgate or dup may be dy itself. */
+ * that y was multiplied with.  A kept value of 2^128, to which a block of fp32's
+ * largest ones may round up, counts as fp32's largest.  dgate or dup may be dy
+ * itself. */
 nc_status nc_act_backward(nc_act act, const nc_plane *dy, nc_dtype dtype, const nc_mx_matrix *gate_q,
                           const nc_mx_matrix *up_q, const nc_plane *dgate, const nc_plane *dup, const nc_plane *y,
                           void *stream);

@@ -48,6 +48,19 @@ template <int ACT> __device__ __forceinline__ void act_of(float z, float& f, flo
   }
 }
 
+// What was kept, as fp32.  Blocks of fp32's largest values (a mask's lowest ones) may round
+// up to 2^128, which is finite but past fp32: it counts as fp32's largest number, one
+// rounding away, so that a factor of 0 next to it gives 0.
+template <int FMT> __device__ __forceinline__ void kept8(u32x2 c, uint32_t sb, float (&y)[8]) {
+  constexpr uint32_t EMAX = FMT == NC_E2M1 ? 2 : FMT == NC_E4M3 ? 8 : 15;
+  decode8<FMT>(c, sb, y);
+  if (sb + EMAX >= 255u) {                       // 2^EMAX 2^(sb - 127) is past fp32
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((__float_as_uint(y[i]) & kAbsMask) == kInfBits) y[i] = copysignf(FLT_MAX, y[i]);
+  }
+}
+
 template <int DT> __device__ __forceinline__ void floats(const Eight<DT>& x, float (&y)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(bits_of<DT>(x, i));
@@ -145,8 +158,8 @@ NC_STREAM_KERNEL act_backward(ActBackward a) {
     const int64_t col = at.col(s0 + s), left = a.gate_q.cols - col;
     float d[8], z[8], w[8], dz[8], dw[8], y[8];
     floats<DT>(dy[s], d);
-    decode8<FMT>(g[s], (sg >> (8 * s)) & 255u, z);
-    if constexpr (GATED) decode8<FMT>(u[s], (su >> (8 * s)) & 255u, w);
+    kept8<FMT>(g[s], (sg >> (8 * s)) & 255u, z);
+    if constexpr (GATED) kept8<FMT>(u[s], (su >> (8 * s)) & 255u, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float f, df;
