@@ -164,7 +164,7 @@ NC_STREAM_KERNEL act_backward(ActBackward a) {
     for (int i = 0; i < 8; ++i) {
       float f, df;
       act_of<ACT>(z[i], f, df);
-      dz[i] = GATED ? d[i] * w[i] * df : d[i] * df;
+      dz[i] = d[i] * (GATED ? w[i] * df : df);   // w df first: d w may pass fp32 where df is 0 or small
       dw[i] = d[i] * f;
       y[i] = GATED ? f * w[i] : f;
     }

@@ -60,6 +60,15 @@ def test_gradients_of_lowest_values(act, fmt, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("act", ACTS)
+def test_steps_whose_product_with_up_passes_fp32(act, fmt, dtype):
+    """dy u is past fp32, dy u f'(g) is not."""
+    t = float(torch.finfo(DT[dtype]).max)
+    gradients([-20.0, -20.0, -200.0, -200.0, -20.0], [t, -t, t, -t, 1e30], [4.0, 4.0, 4.0, -8.0, 1e12], act, fmt, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("fmt", FMTS)
 def test_read_at_every_scale(fmt, dtype):
     """Every value of the grid at every exponent that fp32 has, read as fp32 and as bf16: rounded once below the
     normal range, infinite where a block's largest value rounds up past it."""
