@@ -8,7 +8,7 @@ import torch
 
 import scaled_fp8_casting_amd as nc
 from oracle import mx
-from tests._mx import DT, FMTS, f64, rounded, written
+from tests._mx import DT, FMTS, close, f64, product, rounded, written
 from tests.test_gpu_act import ACTS, bound, like
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +90,28 @@ def test_read_at_every_scale(fmt, dtype):
     with np.errstate(over="ignore"):
         ref = torch.from_numpy(want.astype(np.float32)).to(DT[dtype])
     assert torch.equal(out.cpu(), ref)
+
+
+@pytest.mark.parametrize("m", [3, 700])
+@pytest.mark.parametrize("fa,fb", [("e2m1", "e2m1"), ("e4m3", "e2m1"), ("e5m2", "e4m3")])
+def test_products_of_lowest_values(fa, fb, m):
+    """A column at the type's lowest value against small and zero weights.  The scaled instruction has 2^128 as it is;
+    fp32 results of 8-bit operands have what a matrix reads back as in fp32, an infinity."""
+    rng = np.random.default_rng(1)
+    n, k = 40, 96
+    x, w = rng.standard_normal((m, k)), rng.standard_normal((n, k))
+    x[:, 32:64] = 0                                      # a block of its own
+    x[:, 40] = float(torch.finfo(torch.bfloat16).min)
+    w[:, 32:64] = 0
+    w[::2, 40] = 2.0 ** -100
+    x, w = rounded(x, "bf16"), rounded(w, "bf16")
+    a, b = written(x, fa), written(w, fb)
+    exact = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    nc.nc_mx_matmul(a, b, exact)
+    close(exact, *product(x, w, fa, fb, "bf16"))
+    out = torch.empty(m, n, device="cuda")
+    nc.nc_mx_matmul(a, b, out)
+    if fa == fb == "e2m1":
+        close(out, *product(x, w, fa, fb, "fp32"))
+    else:
+        assert bool((out[:, ::2] == -float("inf")).all()) and bool(out[:, 1::2].isnan().all())
