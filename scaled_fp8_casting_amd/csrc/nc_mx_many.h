@@ -48,22 +48,25 @@ __device__ __forceinline__ const uint8_t* mx_uniform(const uint8_t* p) {
 // A copy of one or two KiB from memory to LDS, 16 bytes a lane from base + off; at:
 // byte of LDS of the first lane's.  Written as assembly because the compiler waits
 // for all copies in flight before any read of LDS; waiting is the caller's.  It has
-// no result that a register would have to be kept for.  M0 holds the LDS address (the
-// compiler never leaves a value in it, and nothing else here uses it), and its write
-// needs a wait state before the use.  The instruction's offset counts in memory and
-// in LDS.
+// no result that a register would have to be kept for.  M0 holds the LDS address; its
+// write needs a wait state before the use.  It is named as clobbered, so that a value
+// that the compiler puts there is written anew after it (M0 is never allocated, of which
+// a warning would tell).  The instruction's offset counts in memory and in LDS.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int UNITS> __device__ __forceinline__ void mx_copy(const uint8_t* base, uint32_t off, uint32_t at) {
   const int m0 = __builtin_amdgcn_readfirstlane((int)at);
   if constexpr (UNITS == 2)
     __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
-                     ::"s"(m0), "v"(off), "s"(mx_uniform(base)) : "memory");
+                     ::"s"(m0), "v"(off), "s"(mx_uniform(base)) : "memory", "m0");
   else
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(mx_uniform(base)) : "memory");
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(mx_uniform(base)) : "memory", "m0");
 }
 // 256 bytes, a dword a lane.
 __device__ __forceinline__ void mx_copy_scales(const uint8_t* base, uint32_t off, uint32_t at) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(off), "s"(mx_uniform(base)) : "memory");
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(off), "s"(mx_uniform(base)) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 template <int N> __device__ __forceinline__ void mx_wait() { __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void mx_barrier() {
   __asm__ volatile("" ::: "memory");
