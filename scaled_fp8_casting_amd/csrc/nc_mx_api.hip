@@ -202,8 +202,9 @@ nc_status nc_mx_read(const nc_mx_matrix* m, const nc_plane* y, nc_dtype dtype, v
 
 size_t nc_mx_workspace_bytes(const nc_mx_matrix* b, int64_t rows, int32_t x_fmt) {
   if (b == nullptr || check_sizes(b->rows, b->cols, b->fmt) != NC_OK || rows < 0 || rows > INT32_MAX) return 0;
+  if (x_fmt >= 0 && rows <= kMxFusedRows) return 0;   // nothing written first, no splits
   const size_t part = most_part_bytes(rows, b->rows, chunks_of(b->cols));
-  if (x_fmt < 0 || rows <= kMxFusedRows) return part;
+  if (x_fmt < 0) return part;
   return check_sizes(rows, b->cols, x_fmt) == NC_OK ? part + round256(bytes_of(rows, b->cols, x_fmt)) : 0;
 }
 
