@@ -105,3 +105,19 @@ def test_one_result_off_16_bytes(at):
     assert torch.equal(dy, want[0]) and torch.equal(got[1], want[1])
     nc.nc_act_forward(gate, up, gate)                    # over gate itself
     assert torch.equal(gate, y)
+
+
+@pytest.mark.parametrize("rows", [70, ROWS])             # single steps, whole chunks
+def test_over_their_own_inputs(rows):
+    """y over up, dup over dy."""
+    gate, up, dy = (x[:rows] for x in planes(3, "bf16", 4104, seed=8))
+    gq, uq = nc.new_mx_matrix(rows, COLS, "e5m2"), nc.new_mx_matrix(rows, COLS, "e5m2")
+    y, dg, du = (torch.empty(rows, COLS, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    nc.nc_act_forward(gate, up, y, gq, uq, act="gelu")
+    nc.nc_act_backward(dy, gq, uq, dg, du, act="gelu")
+    kept = value(uq)
+    nc.nc_act_forward(gate, up, up, gq, uq, act="gelu")
+    assert torch.equal(up, y) and torch.equal(value(uq), kept)
+    got = torch.empty_like(dg)
+    nc.nc_act_backward(dy, gq, uq, got, dy, act="gelu")
+    assert torch.equal(dy, du) and torch.equal(got, dg)

@@ -188,3 +188,54 @@ def test_graphs_of_split_products_share_a_workspace():
         torch.cuda.synchronize()
         for x, o in zip(xs, outs):
             assert torch.equal(o, (x.double() @ w.double().T).float())
+
+
+def test_columns_up_to_31_bits():
+    """The longest rows: 2^31 - 1 columns, in splits and quantised on the way."""
+    k, m, n = 2 ** 31 - 1, 12, 5
+    at = torch.tensor([0, 255, 256, 2 ** 30 + 7, 2 ** 31 - 300, 2 ** 31 - 2], device="cuda")
+    x, y = (torch.zeros(k, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[at] = torch.tensor([1, 2, -3, 4, 6, 3.0], device="cuda").bfloat16()
+    y[at] = torch.tensor([4, -1, 2, 3, 1, -6.0], device="cuda").bfloat16()
+    want = float((x[at].float() * y[at].float()).sum())
+    b = nc.new_mx_matrix(n, k)
+    nc.nc_mx_write(y[None].expand(n, k), b)
+    del y
+    out = full(3, n, "bf16")
+    nc.nc_mx_linear(x[None].expand(3, k), b, out, fmt="e2m1")
+    assert bool((out == want).all())
+    a = nc.new_mx_matrix(m, k)
+    nc.nc_mx_write(x[None].expand(m, k), a)
+    for dtype in ANY:
+        out = full(m, n, dtype)
+        nc.nc_mx_matmul(a, b, out)
+        assert bool((out == want).all())
+
+
+def test_workspace_from_torch_on_any_stream():
+    """ws=None where splits need one: streams given as objects and by number, the default one's 0, under capture too."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, w = whole(g, 100, 20000), whole(g, 130, 20000)
+    a, b = written(x, "e4m3"), written(w, "e4m3")
+    want = (x.double() @ w.double().T).float()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for stream in (None, 0, side, side.cuda_stream):
+        out = full(100, 130, "fp32")
+        torch.cuda.synchronize()
+        nc.nc_mx_matmul(a, b, out, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    out = full(100, 130, "fp32")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nc.nc_mx_matmul(a, b, out)
+    for _ in range(3):
+        out.zero_()
+        junk = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(8)]     # eager work between the replays
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del junk
