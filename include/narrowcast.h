@@ -513,7 +513,9 @@ size_t nc_mx_bytes(int64_t rows, int64_t cols, int32_t fmt);
 /* Quantises x [rows, cols] into m (nullable), with blocks along x's rows, and
  * into t (nullable), the transposed matrix [cols, rows] with blocks down x's
  * columns: what the products of a backward pass take.  One of them at least; both
- * of one format and from one read of x.  All of data is written. */
+ * of one format and from one read of x.  All of data is written.  t is limited
+ * further, which matters to x of few columns alone: (t->rows / 256) * (t->cols /
+ * 256), each rounded up, at most 2^22 - 9, else NC_E_ARG. */
 nc_status nc_mx_write(const nc_mx_matrix *m, const nc_mx_matrix *t, const nc_plane *x, nc_dtype dtype,
                       nc_mx_rule rule, void *stream);
 
@@ -569,7 +571,8 @@ typedef enum { NC_ACT_SILU = 0, NC_ACT_GELU = 1, NC_ACT_GELU_TANH = 2, NC_ACT_RE
 
 /* Forward over [rows, cols]: y from gate and up (nullable), which are also
  * quantised into gate_q and up_q (matrices [rows, cols] of one format, as by
- * nc_mx_write) -- all that a backward pass needs.  gate_q NULL keeps nothing
+ * nc_mx_write) -- all that a backward pass needs.  Sizes are those of a matrix,
+ * kept or not.  gate_q NULL keeps nothing
  * (up_q then too); otherwise up_q goes with up.  y may be gate or up itself. */
 nc_status nc_act_forward(nc_act act, int64_t rows, int64_t cols, const nc_plane *gate, const nc_plane *up,
                          const nc_plane *y, nc_dtype dtype, const nc_mx_matrix *gate_q, const nc_mx_matrix *up_q,

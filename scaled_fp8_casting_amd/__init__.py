@@ -749,7 +749,8 @@ def _named(name, names: dict, what: str) -> int:
 
 def nc_mx_write(x: torch.Tensor, m: Optional[MxMatrix] = None, t: Optional[MxMatrix] = None, rule="ceil", stream=None):
     """Quantise x [rows, cols] (fp32 or bf16, any row stride) into m, with blocks along its rows, and into t, the
-    transposed matrix [cols, rows] with blocks down its columns; one of them or, from one read of x, both."""
+    transposed matrix [cols, rows] with blocks down its columns; one of them or, from one read of x, both.  With t,
+    (rows / 256) * (cols / 256), each rounded up, is at most 2^22 - 9."""
     code, r, md, td = _element(x.dtype, "x"), _named(rule, MX_RULE, "rule"), None, None
     if m is not None:
         md, one, rows, cols = m.descriptor, m, m._rows, m._cols   # descriptor first: it looks at data anew

@@ -75,8 +75,18 @@ template <int DT> __device__ __forceinline__ uint8_t* row_of(const Plane<void*>&
 // STEPS: how many of a chunk's four steps a workgroup takes.  One where there would be
 // few workgroups of four: a thread's elements follow each other, and their functions
 // are long.  In us, with four and with one: gelu over 1001 x 1365 fp32 9.5 and 7.2,
-// gelu_tanh's gradient over 100 x 4096 7.1 and 3.6, gelu gated over 4096 x 4096 bf16
-// 38.2 and 36.7, silu gated over 8192 x 11008 159 and 174.
+// gelu_tanh's gradient over 100 x 4096 7.1 and 3.6; over rows of 4096 columns, gated, E4M3,
+// replayed from a graph:
+//   chunks                  512         1024         2048         4096         8192        16384
+//   silu    bf16       13.6 12.7    20.5 19.2    32.6 30.6    57.4 57.1   104.3 109.5  197.2 218.6
+//   gelu    bf16       16.2 14.8    25.3 23.2    39.7 38.0    72.7 72.0   131.6 138.9  255.1 269.8
+//   relu2   bf16       11.2 10.8    17.7 18.0    29.1 31.9    53.7 59.6   102.1 115.1  196.0 228.7
+//   gelu    fp32       19.1 16.7    30.3 27.7    52.5 51.3    93.9 96.9   175.9 188.5  346.0 376.9
+//   gradient, y again:
+//   silu    bf16       15.0 12.6    21.5 21.8    37.2 36.6    66.8 72.0   127.8 139.6  249.8 276.2
+//   gelu    bf16       17.8 15.4    26.9 25.5    41.5 43.1    78.0 80.6   147.9 156.1  282.7 304.0
+//   relu2   bf16       12.2 13.0    21.2 20.9    34.3 35.9    64.8 70.3   124.0 137.8  251.6 274.0
+// One number for all: relu2 would gain 3 us at 2048 chunks from four, silu loses 2.
 template <int STEPS> struct ActPart {
   int s0;
   MxLane at;
@@ -191,7 +201,7 @@ template <typename Fn> hipError_t by_act(int act, int fmt, int dtype, Fn fn) {
   return hipErrorInvalidValue;
 }
 
-constexpr uint32_t kFewChunks = 4096;
+constexpr uint32_t kFewChunks = 4096;              // measured above
 
 // fn(steps of a workgroup as a constant, workgroups)
 template <typename Fn> void by_steps(const MxMat& m, Fn fn) {

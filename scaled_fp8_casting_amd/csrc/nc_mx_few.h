@@ -184,7 +184,8 @@ template <int FA, int FB, bool WIDE> hipError_t mx_few_run(const MxProduct& p, i
   if (p.x == nullptr) return t == 2 ? mx_few_go<FA, FB, WIDE, kMxNoRows, 2, 8>(p, stream) : mx_few_go<FA, FB, WIDE, kMxNoRows, 1, 8>(p, stream);
   // With a compute unit for each workgroup, sixteen waves take in more at once (1 x
   // 11008 -> 4096, 4 by 4 bits: 9.2 us against 11.4); two matrices' operands do not fit
-  // their registers (32 x 11008 -> 4096 of 8 by 8 bits: 30 us against 20).
+  // their registers (32 x 11008 -> 4096 of 8 by 8 bits, called one by one: 30 us against 20 with eight
+  // waves, which take 16.2 replayed from a graph).
   // So it is for 8 bits through bf16.
   constexpr int MORE = WIDE && FB != NC_E2M1 ? 8 : 16;
   if (p.b.strips <= 256 && p.b.chunks > 8)

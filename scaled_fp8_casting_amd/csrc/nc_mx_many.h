@@ -24,11 +24,15 @@
 // runs of 1 KiB and meet no bank twice.  Scales go the same way, a dword a lane and
 // chunk, a chunk ahead of their codes.
 //
-// What bounds it is power: with all compute units at the products alone the clock
-// is 1.46 GHz (E2M1), and the copies and reads take a third of the time more
-// (4096 x 4096 x 16384 E2M1: a stage 0.96 us, 0.70 with the products alone).  8192^3
-// once the power control has settled: E2M1 241 .. 247 us, 4.5 PFLOP/s; E4M3 375 .. 383,
-// 2.9; to fp32 through bf16 890 .. 907.  The first 8 ms of a load: 274, 440, 990.
+// What bounds large ones is power, then what the matrix units wait for: counters give
+// a clock of 1.6 to 1.75 GHz in place of 2.4 and matrix units that are busy for 64%
+// (8192^3 E2M1), 78% (E4M3), 68% (to fp32 through bf16), 76% (4096 x 4096 x 65536 E2M1),
+// 83% (4096 x 4096 x 16384 E5M2 x E4M3) of the cycles; 4096 x 11008 over 4096
+// columns 47% at 1.89 GHz: the beginning and end of sixteen chunks weigh more, and the last
+// of three rounds is not full.  With the products
+// alone left in a copy of the kernel a stage of E2M1 takes 0.70 us of 0.96.  8192^3 once
+// the power control has settled: E2M1 231 .. 247 us, 4.5 PFLOP/s; E4M3 375 .. 399, 2.8;
+// to fp32 through bf16 890 .. 907.  The first 8 ms of a load: 274, 440, 990.
 #pragma once
 
 #include <type_traits>

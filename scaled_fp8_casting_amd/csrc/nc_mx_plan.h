@@ -34,7 +34,9 @@ constexpr int64_t kSplitChunks = 4;              // fewest chunks of a split
 //                 512 x 4096 x 4096   18.1  13.4  13.6   27.7   26.6
 //                2048 x 2048 x 2048   21.3  16.6  10.3   19.4   35.5
 //                4096 x 4096 x 4096                46.5   41.7
-//   E4M3 x E4M3   256 x 4096 x 4096   21.2  13.3  21.9   43.8   19.7
+//   E4M3 x E4M3    32 x 4096 x 4096    6.1   9.0  14.6          11.6
+//                  32 x 4096 x 11008  16.2  26.4  46.9          21.4   (8 splits 19.3; the estimate says 14.0)
+//                 256 x 4096 x 4096   21.2  13.3  21.9   43.8   19.7
 //                1024 x 1024 x 16384  61.9  35.9  75.6  143.8   32.6
 //                4096 x 4096 x 4096                75.5   61.9
 //   to fp32, E4M3 x E2M1
