@@ -28,7 +28,10 @@ constexpr int64_t kSplitChunks = 4;              // fewest chunks of a split
 // Fitted to 17 sizes of 33 .. 2048 x 256 .. 11008 x 1024 .. 16384 in each class and
 // checked at 70 drawn ones (2 .. 8192 x 40 .. 11008 x 70 .. 16384): the choice was
 // within 10% of the fastest in all but those where a launch is most of the time and
-// one at 16% (253 x 9025 x 9741 E4M3 x E2M1: 47 us against 40.5 in 3 splits).
+// one at 16% (253 x 9025 x 9741 E4M3 x E2M1: 47 us against 40.5 in 3 splits).  At 70
+// others (profiles/mx_plans.txt) it was within 4% in 67 and 8, 26 and 27% off in three:
+// 5411 x 5679 x 1884 E4M3 x E2M1 takes 82 us at 256 a side and 65 at 128, 485 x 614 x
+// 9311 E4M3 23 us with 1 strip and 18 with 2.
 // Some of them, in us (1 strip, 2 strips, 128 a side, 256 a side, 128 in 4 splits):
 //   E2M1 x E2M1    64 x 4096 x 4096    5.6   9.5  12.4          12.0
 //                 512 x 4096 x 4096   18.1  13.4  13.6   27.7   26.6
